@@ -134,8 +134,23 @@ __device__ __forceinline__ uint4 ld_hint(const uint4* p, uint64_t policy) {
     return v;
 }
 
+// 16 bytes that are not read again. Coherent, and kept in program order: a
+// programmatic dependent is resident while the launch before it may still be
+// writing what it will read, so such data takes no .nc load (which asks for
+// memory that is read-only for the kernel's whole life, and which the compiler
+// may move above the wait of dependent_start).
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // Start of every kernel launched by launch_kernel: let the next kernel begin
-// launching, then wait until everything before this one has completed.
+// launching, then wait until everything before this one has completed. What
+// comes after is read by plain loads or those above, never by __ldg.
 __device__ __forceinline__ void dependent_start() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");

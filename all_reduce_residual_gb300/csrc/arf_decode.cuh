@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
             if (one_page ? (n_mask & (0xffffu << (lane & (TOK - 16)))) != 0 : ((n_mask >> lane) & 1u) != 0) {
                 const uint32_t page = p.page.div((uint32_t)tok);
                 n_row = tok - (int)(page * p.page.d);
-                n_page = __ldg(p.table + (int64_t)pb * p.table_stride + page);
+                n_page = p.table[(int64_t)pb * p.table_stride + page];
             }
         }
         n_item = pb * p.per_seq + p_item;
@@ -562,10 +562,10 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 if constexpr (ES == 2) {
-                    qf[n][ks][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + ks * 16 + 2 * t)) : 0u;
-                    qf[n][ks][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + 2 * t)) : 0u;
+                    qf[n][ks][0] = live ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 2 * t) : 0u;
+                    qf[n][ks][1] = live ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + 2 * t) : 0u;
                 } else {
-                    const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(q + ks * 16 + 4 * t)) : make_uint2(0u, 0u);
+                    const uint2 w = live ? *reinterpret_cast<const uint2*>(q + ks * 16 + 4 * t) : make_uint2(0u, 0u);
                     qf[n][ks][0] = w.x, qf[n][ks][1] = w.y;
                 }
             }

@@ -17,7 +17,6 @@
 #include <vector>
 
 #include "arf_attn.cuh"
-#include "arf_kernels.cuh"
 
 namespace arf {
 namespace {
@@ -63,7 +62,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
             const uint32_t outer = p.d_inner.div(run);
             at[i] = (int64_t)outer * p.outer_stride + (int64_t)(run - outer * p.d_inner.d) * p.inner_stride +
                     (int64_t)(c - (int)(run * p.d_run.d)) * 16;
-            v[i] = ld_once(reinterpret_cast<const uint4*>(src + at[i]));
+            v[i] = ld_stream(reinterpret_cast<const uint4*>(src + at[i]));
         }
     }
 #pragma unroll

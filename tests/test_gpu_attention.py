@@ -886,3 +886,48 @@ def test_decode_step_between_two_epilogues(ws, dtype, W):
     x = ro.cpu().double()
     norm = x / (x.square().mean(-1, keepdim=True) + eps).sqrt() * gamma.double()
     ref.assert_close(y, norm, 2 * ref.half_step(norm * 1.01, dtype), "out")
+
+
+# ---- what the launch before has written ------------------------------------------
+
+
+@pytest.mark.parametrize("width", [4, 4000])
+def test_replayed_append_copy_and_decode(ws, width):
+    """Append, page copy and attention back to back in one graph, each reading
+    what the launch before it wrote, with other data in every replay."""
+    page, H, G, D, B = 8, 2, 4, 64, 4
+    n = page  # one page per sequence, filled by the append and copied
+    kp, vp = (torch.zeros(2 * B, page, H, D, dtype=BF16, device=DEV) for _ in range(2))
+    cache = arf.KVCache(kp, vp)
+    q, k, v = (torch.zeros(B * n, h, D, dtype=BF16, device=DEV) for h in (H * G, H, H))
+    pos = torch.arange(B * n, dtype=torch.int32, device=DEV) % n
+    slots = torch.arange(B * n, device=DEV)
+    table = torch.full((B, width), -1, dtype=torch.int32)
+    table[:, 0] = torch.arange(B, 2 * B)
+    table, lens = table.to(DEV), torch.full((B,), n, dtype=torch.int32, device=DEV)
+    size = ctypes.c_size_t()
+    assert arf.arf_paged_decode_scratch_bytes(ws.handle, cache.struct, B, H * G, width, 0, size) == arf.ARF_OK
+    assert (size.value > 0) == (width == 4000), "both forms are meant"
+    rot = arf.RotaryTable(D)
+
+    def step():
+        qr = arf.rotary_append(ws, q, k, v, pos, slots, rot, cache)
+        arf.copy_pages(ws, cache, list(range(B)), list(range(B, 2 * B)))
+        last = qr[n - 1::n]
+        return last, arf.paged_decode(ws, last, cache, table, lens)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        last, got = step()
+    for it in range(20):
+        for x, seed in ((q, 1), (k, 2), (v, 3)):
+            x.copy_(randn(tuple(x.shape), BF16, 10 * it + seed))
+        g.replay()
+        torch.cuda.synchronize()
+        assert same(vp[:B].flatten(0, 1), v) and same(vp[B:], vp[:B]) and same(kp[B:], kp[:B])
+        want, bound = ref.rotate(k.cpu(), pos.cpu(), inv_freq(D), D, False)
+        ref.assert_close(kp[B:].flatten(0, 1), want, bound + ref.half_step(want, BF16))
+        ref.assert_decode(got, ref.decode(last.cpu(), kp.cpu(), vp.cpu(), "nhd", table[:, :1].cpu(), lens.cpu(),
+                                          D ** -0.5), BF16, f"replay {it}")
