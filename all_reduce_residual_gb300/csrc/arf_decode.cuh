@@ -200,6 +200,27 @@ __device__ __forceinline__ void send2(uint32_t at, const float2& v, uint32_t bar
                  : "memory");
 }
 
+// Wait for phase 0 of this CTA's barrier that other CTAs' stores complete on;
+// false once `limit` SM cycles have passed. Those stores release at cluster
+// scope, so the wait acquires there (without a scope it would be the CTA's).
+__device__ __forceinline__ bool cluster_wait_bounded(uint32_t bar, long long limit) {
+    const auto arrived = [&]() {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar)
+            : "memory");
+        return done != 0;
+    };
+    const long long t0 = clock64();
+    while (!arrived())
+        if (clock64() - t0 > limit) return false;
+    return true;
+}
+
 // tanh(z) = 1 - 2 / (1 + e^2z), off by 2^-22 or so; below 1/4, where that
 // would be much of the value, its series to z^9 (the term left out is below
 // 2^-26 of the value).
@@ -936,10 +957,10 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
     __syncthreads();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&s_bar);
-    if (!mbar_wait_bounded(bar, 0, kBulkSpinLimit)) {
+    if (!cluster_wait_bounded(bar, kBulkSpinLimit)) {
         // never seen: count it, give what is on its way as long again, and
         // leave without an answer
-        (void)mbar_wait_bounded(bar, 0, kBulkSpinLimit);
+        (void)cluster_wait_bounded(bar, kBulkSpinLimit);
         if (threadIdx.x == 0) atomicAdd(p.timeouts, 1u);
         return;
     }

@@ -931,3 +931,30 @@ def test_replayed_append_copy_and_decode(ws, width):
         ref.assert_close(kp[B:].flatten(0, 1), want, bound + ref.half_step(want, BF16))
         ref.assert_decode(got, ref.decode(last.cpu(), kp.cpu(), vp.cpu(), "nhd", table[:, :1].cpu(), lens.cpu(),
                                           D ** -0.5), BF16, f"replay {it}")
+
+
+def test_clusters_join_what_arrives(ws):
+    """Clusters of every size, many times over with other data: the first CTA
+    of each reads what the others sent, not what was there before."""
+    D, Hkv, G = 128, 1, 4
+    for tokens in (100, 200, 500, 1000):
+        cases = [batch([tokens, tokens - 7], 16, Hkv, G, D, BF16, BF16, "nhd", seed=s) for s in range(4)]
+        size = ctypes.c_size_t()
+        held = []
+        for q, kp, vp, table, n in cases:
+            cache = arf.KVCache(kp.to(DEV), vp.to(DEV))
+            st = arf.arf_paged_decode_scratch_bytes(ws.handle, cache.struct, 2, G, table.shape[1], 0, size)
+            assert (st, size.value) == (arf.ARF_OK, 0), "the cluster form is meant"
+            held.append((q.to(DEV), cache, table.to(DEV), n.to(DEV)))
+        got = [[arf.paged_decode(ws, *a) for a in held] for _ in range(50)]
+        for i, (q, kp, vp, table, n) in enumerate(cases):
+            ref.assert_decode(got[0][i], ref.decode(q, kp, vp, "nhd", table, n, D ** -0.5), BF16, f"{tokens}")
+            for again in got[1:]:
+                assert same(again[i][0], got[0][i][0]) and same(again[i][1], got[0][i][1])
+    assert wait_timeouts(ws) == 0
+
+
+def wait_timeouts(ws):
+    n = ctypes.c_uint()
+    assert arf.arf_workspace_wait_timeouts(ws.handle, n) == arf.ARF_OK
+    return n.value
