@@ -10,7 +10,10 @@ A decode step of a layer, between two epilogues (``run``)::
 
 Like ``run``, these functions check shapes, dtypes and devices, allocate
 outputs and scratch through torch, and pass torch's current stream (or
-``stream``); everything else happens in libarf.so's kernels. Nothing is read
+``stream``); everything else happens in libarf.so's kernels. With ``stream``,
+outputs and scratch come from that stream's memory, so that nothing queued
+elsewhere still uses them; the caller orders what the call reads, and what
+later reads its outputs, as between any two streams. Nothing is read
 back, so they can be captured into CUDA graphs. The checks and the call itself
 are in the module _torch_ops (csrc/torch_ops.cpp), for the host's time. No
 gradients are recorded.

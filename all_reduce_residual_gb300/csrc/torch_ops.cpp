@@ -12,6 +12,7 @@
 #include <c10/core/Allocator.h>
 #include <c10/core/StorageImpl.h>
 #include <c10/core/TensorImpl.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -82,14 +83,49 @@ const void* index(PyObject* o, const char* name, ScalarType dtype, int device, i
     return t.data_ptr();
 }
 
-// Memory of torch's caching allocator on the current device and stream (the
-// library refuses another device than the current one), and a contiguous
-// tensor in it. What torch.empty does, without its dispatch.
-c10::Storage memory(size_t bytes) {
-    c10::Allocator* allocator = c10::GetAllocator(c10::DeviceType::CUDA);
-    return c10::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes,
-                                                              allocator->allocate(bytes), allocator, true));
-}
+// The stream of a call: the current one, or the given torch stream.
+class Stream {
+  public:
+    Stream(PyObject* given, int device) : device_(device) {
+        const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device);
+        raw_ = current_ = current.stream();
+        if (none(given)) return;
+        PyObject* raw = PyObject_GetAttrString(given, "cuda_stream");
+        if (!raw) throw python_error();
+        raw_ = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(raw));
+        Py_DECREF(raw);
+        if (PyErr_Occurred()) throw python_error();
+    }
+    // Memory of torch's caching allocator, from the pool of the stream that
+    // will write it: what was freed on another stream may still be in use by
+    // work queued there. On the current device, or a given stream's (the
+    // library refuses another device than the current one).
+    c10::Storage memory(size_t bytes) const {
+        if (raw_ == current_) return allocate(bytes);
+        const c10::cuda::CUDAStreamGuard guard(of(raw_));
+        return allocate(bytes);
+    }
+    // An output: it may also be read on the current stream, until it is freed.
+    void shared(const Tensor& t) const {
+        if (raw_ != current_ && t.defined()) t.record_stream(of(current_).unwrap());
+    }
+    void* raw() const { return raw_; }
+
+  private:
+    static c10::Storage allocate(size_t bytes) {
+        c10::Allocator* allocator = c10::GetAllocator(c10::DeviceType::CUDA);
+        return c10::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes,
+                                                                  allocator->allocate(bytes), allocator, true));
+    }
+    c10::cuda::CUDAStream of(cudaStream_t s) const {
+        return c10::cuda::getStreamFromExternal(s, (c10::DeviceIndex)device_);
+    }
+    int device_;
+    cudaStream_t raw_ = nullptr, current_ = nullptr;
+};
+
+// A contiguous tensor in memory of a call's stream. What torch.empty does,
+// without its dispatch.
 Tensor part(c10::Storage storage, at::IntArrayRef size, ScalarType dtype, size_t offset) {
     auto impl = c10::make_intrusive<c10::TensorImpl>(std::move(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA),
                                                      c10::scalarTypeToTypeMeta(dtype));
@@ -100,7 +136,9 @@ Tensor part(c10::Storage storage, at::IntArrayRef size, ScalarType dtype, size_t
 size_t bytes_of(at::IntArrayRef size, ScalarType dtype) {
     return (size_t)c10::multiply_integers(size) * c10::elementSize(dtype);
 }
-Tensor empty(at::IntArrayRef size, ScalarType dtype) { return part(memory(bytes_of(size, dtype)), size, dtype, 0); }
+Tensor empty(const Stream& stream, at::IntArrayRef size, ScalarType dtype) {
+    return part(stream.memory(bytes_of(size, dtype)), size, dtype, 0);
+}
 
 // Two contiguous tensors in one allocation, the second 256-byte aligned: the
 // allocator's time per call is most of a small call's. They are views of one
@@ -108,39 +146,12 @@ Tensor empty(at::IntArrayRef size, ScalarType dtype) { return part(memory(bytes_
 struct Pair {
     Tensor first, second;
 };
-Pair empty_pair(at::IntArrayRef size0, ScalarType dtype0, at::IntArrayRef size1, ScalarType dtype1) {
+Pair empty_pair(const Stream& stream, at::IntArrayRef size0, ScalarType dtype0, at::IntArrayRef size1,
+                ScalarType dtype1) {
     const size_t at = (bytes_of(size0, dtype0) + 255) & ~(size_t)255;
-    const c10::Storage all = memory(at + bytes_of(size1, dtype1));
+    const c10::Storage all = stream.memory(at + bytes_of(size1, dtype1));
     return {part(all, size0, dtype0, 0), part(all, size1, dtype1, at)};
 }
-
-// The stream of a call: the current one, or the given torch stream; tensors
-// made here must then outlive the work there.
-class Stream {
-  public:
-    Stream(PyObject* given, int device) : device_(device) {
-        if (none(given)) {
-            raw_ = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
-            return;
-        }
-        PyObject* raw = PyObject_GetAttrString(given, "cuda_stream");
-        if (!raw) throw python_error();
-        raw_ = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(raw));
-        Py_DECREF(raw);
-        if (PyErr_Occurred()) throw python_error();
-        other_ = true;
-    }
-    void keep(const Tensor& t) const {
-        if (other_ && t.defined())
-            t.record_stream(c10::cuda::getStreamFromExternal(raw_, (c10::DeviceIndex)device_).unwrap());
-    }
-    void* raw() const { return raw_; }
-
-  private:
-    int device_;
-    cudaStream_t raw_ = nullptr;
-    bool other_ = false;
-};
 
 // The C struct behind a handle object of attention.py: its attribute `key`
 // is (address of the struct, device index).
@@ -198,10 +209,10 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     arf_heads_t qo;
     if (none(a[6])) {
         if (has_k && none(a[7])) {
-            Pair made = empty_pair(q.sizes(), st, tensor(a[3], "k").sizes(), st);
+            Pair made = empty_pair(stream, q.sizes(), st, tensor(a[3], "k").sizes(), st);
             q_out = std::move(made.first), k_out = std::move(made.second);
         } else {
-            q_out = empty(q.sizes(), st);
+            q_out = empty(stream, q.sizes(), st);
         }
         qo = {q_out.data_ptr(), qh.heads * D, D, qh.heads};
     } else {
@@ -209,7 +220,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (has_k) {
         if (none(a[7])) {
-            if (!k_out.defined()) k_out = empty(tensor(a[3], "k").sizes(), st);
+            if (!k_out.defined()) k_out = empty(stream, tensor(a[3], "k").sizes(), st);
             ko = {k_out.data_ptr(), kh.heads * D, D, kh.heads};
         } else {
             ko = heads(tensor(a[7], "k_out"), "k_out", st, device, T, kh.heads, D);
@@ -217,8 +228,8 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
         TORCH_CHECK_VALUE(none(a[7]), "k_out without k");
     }
-    stream.keep(q_out);
-    stream.keep(k_out);
+    stream.shared(q_out);
+    stream.shared(k_out);
     const arf_status_t r = arf_rotary(workspace(a[0]), table, static_cast<const int32_t*>(pos), T, (int)D, dt, &qh, &qo,
                                       has_k ? &kh : nullptr, has_k ? &ko : nullptr, stream.raw());
     if (r != ARF_OK) return status(r);
@@ -262,9 +273,9 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor& q = tensor(a[2], "q");
         qh = heads(q, "q", st, device, T, -1, D);
         if (none(a[9])) {
-            q_out = empty(q.sizes(), st);
+            q_out = empty(stream, q.sizes(), st);
             qo = {q_out.data_ptr(), qh.heads * D, D, qh.heads};
-            stream.keep(q_out);
+            stream.shared(q_out);
         } else {
             qo = heads(tensor(a[9], "q_out"), "q_out", st, device, T, qh.heads, D);
         }
@@ -310,21 +321,21 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     arf_heads_t oh;
     if (none(a[9])) {
         if (none(a[10])) {
-            Pair made = empty_pair(q.sizes(), st, {B, (int64_t)qh.heads}, ScalarType::Float);
+            Pair made = empty_pair(stream, q.sizes(), st, {B, (int64_t)qh.heads}, ScalarType::Float);
             out = std::move(made.first), lse = std::move(made.second);
         } else {
-            out = empty(q.sizes(), st);
+            out = empty(stream, q.sizes(), st);
         }
         oh = {out.data_ptr(), qh.heads * D, D, qh.heads};
-        stream.keep(out);
+        stream.shared(out);
     } else {
         oh = heads(tensor(a[9], "out"), "out", st, device, B, qh.heads, D);
     }
     float* lse_ptr;
     if (none(a[10])) {
-        if (!lse.defined()) lse = empty({B, qh.heads}, ScalarType::Float);
+        if (!lse.defined()) lse = empty(stream, {B, qh.heads}, ScalarType::Float);
         lse_ptr = static_cast<float*>(lse.data_ptr());
-        stream.keep(lse);
+        stream.shared(lse);
     } else {
         const Tensor& l = tensor(a[10], "lse");
         TORCH_CHECK_VALUE(l.scalar_type() == ScalarType::Float && l.dim() == 2 && l.size(0) == B &&
@@ -333,17 +344,15 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         on_device(l, "lse", device);
         lse_ptr = static_cast<float*>(l.data_ptr());
     }
-    // scratch of the caching allocator (512-byte aligned): later work on this
-    // stream may reuse it, work on other streams may not
+    // scratch of the caching allocator (512-byte aligned), from the pool of
+    // the call's stream: work before and after it there may use the same
+    // memory, work on other streams may not
     size_t bytes = 0;
     const arf_status_t need =
         arf_paged_decode_scratch_bytes(workspace(a[0]), cache, B, qh.heads, (int32_t)width, window, &bytes);
     if (need != ARF_OK) return status(need);
     Tensor scratch;
-    if (bytes > 0) {
-        scratch = empty({(int64_t)bytes}, ScalarType::Byte);
-        stream.keep(scratch);
-    }
+    if (bytes > 0) scratch = empty(stream, {(int64_t)bytes}, ScalarType::Byte);
     const arf_status_t r =
         arf_paged_decode(workspace(a[0]), cache, B, dt, &qh, static_cast<const int32_t*>(table.data_ptr()),
                          B > 1 ? table.stride(0) : width, (int32_t)width, static_cast<const int32_t*>(lens), scale, cap,

@@ -958,3 +958,66 @@ def wait_timeouts(ws):
     n = ctypes.c_uint()
     assert arf.arf_workspace_wait_timeouts(ws.handle, n) == arf.ARF_OK
     return n.value
+
+
+def pool_stream(t):
+    """The stream in whose pool of the caching allocator a tensor lies."""
+    at = t.untyped_storage().data_ptr()
+    return [s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"]][0]
+
+
+def test_outputs_on_another_stream_lie_in_its_memory(ws):
+    q, k = (randn((5, h, 64), BF16, h).to(DEV) for h in (4, 2))
+    pos = torch.arange(5, dtype=torch.int32, device=DEV)
+    cache = arf.KVCache(*(torch.zeros(4, 16, 2, 64, dtype=BF16, device=DEV) for _ in range(2)))
+    table, lens = torch.zeros(5, 1, dtype=torch.int32, device=DEV), pos + 1
+    rot = arf.RotaryTable(64)
+    torch.cuda.synchronize()
+    here, s = torch.cuda.current_stream(), torch.cuda.Stream()
+    for stream, where in ((None, here), (here, here), (s, s)):
+        made = [*arf.rotary(ws, q, k, pos, rot, stream=stream), arf.rotary(ws, q, None, pos, rot, stream=stream)[0],
+                arf.rotary_append(ws, q, k, k, pos, pos.long(), rot, cache, stream=stream)]
+        if stream is s:
+            s.synchronize()
+        made += arf.paged_decode(ws, q, cache, table, lens, stream=stream)
+        made += [arf.paged_decode(ws, q, cache, table, lens, lse=made[-1], stream=stream)[0]]
+        assert {pool_stream(x) for x in made} == {where.cuda_stream}
+        torch.cuda.synchronize()
+
+
+def test_memory_in_use_elsewhere_is_not_written(ws):
+    """A call on another stream while work queued on the current one still
+    reads tensors that were freed: neither its outputs nor its scratch are
+    theirs."""
+    Hkv, G, D, B = 1, 4, 64, 4
+    q, kp, vp, table, n = batch([5000, 17, 0, 300], 16, Hkv, G, D, BF16, BF16, "nhd", width=4000)
+    want = ref.decode(q, kp, vp, "nhd", table[:, :320], n, D ** -0.5)
+    cache = arf.KVCache(kp.to(DEV), vp.to(DEV))
+    q, table, n = q.to(DEV), table.to(DEV), n.to(DEV)
+    size = ctypes.c_size_t()
+    assert arf.arf_paged_decode_scratch_bytes(ws.handle, cache.struct, B, Hkv * G, table.shape[1], 0, size) == arf.ARF_OK
+    assert size.value > 0, "the form with scratch is meant"
+    s = torch.cuda.Stream()
+    for warm in range(3):  # modules loaded, pools filled
+        arf.paged_decode(ws, q, cache, table, n, stream=s)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    sizes = [size.value, B * Hkv * G * D * 2 + 256, B * Hkv * G * D * 2 + B * Hkv * G * 4, 1 << 20]
+    kept = [torch.empty(x, dtype=torch.uint8, device=DEV) for x in sizes]
+    temps = [torch.full((x,), 91, dtype=torch.uint8, device=DEV) for x in sizes]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    for x, y in zip(temps, kept):
+        y.copy_(x)
+    freed = {x.data_ptr() for x in temps}
+    del temps, x
+    got = [arf.paged_decode(ws, q, cache, table, n, stream=s) for _ in range(8)]
+    busy = not torch.cuda.current_stream().query()
+    again = [torch.empty(x, dtype=torch.uint8, device=DEV).data_ptr() for x in sizes]
+    torch.cuda.synchronize()
+    assert busy, "the calls were made after the work on the current stream had ended"
+    assert freed & set(again), "nothing that was freed could have been handed out"
+    for y in kept:
+        assert bool((y == 91).all())
+    for g in got:
+        ref.assert_decode(g, want, BF16)
