@@ -175,8 +175,20 @@ def run(ws: Workspace, pattern, partials, residual=None, gamma=None, eps: float 
         if ldp is not None and ld != ldp:
             raise ValueError("all partials must have the same row stride")
         ldp = ld
+
+    def made():
+        """An output in memory of the call's stream: what was freed on another
+        stream may still be in use by work queued there."""
+        if stream is None:
+            return torch.empty((M, H), dtype=dt, device=dev)
+        with torch.cuda.stream(stream):
+            t = torch.empty((M, H), dtype=dt, device=dev)
+        if M > 0:
+            t.record_stream(torch.cuda.current_stream(dev))  # on which it may be read next
+        return t
+
     if out is None:
-        out = torch.empty((M, H), dtype=dt, device=dev)
+        out = made()
     ldo = _check_operand(out, "out", (M, H), dt, dev)
     r_ptr = g_ptr = ro_ptr = None
     ldr = ldro = H
@@ -186,7 +198,7 @@ def run(ws: Workspace, pattern, partials, residual=None, gamma=None, eps: float 
         ldr = _check_operand(residual, "residual", (M, H), dt, dev)
         _check_operand(gamma, "gamma", (H,), dt, dev)
         if residual_out is None:
-            residual_out = torch.empty((M, H), dtype=dt, device=dev)
+            residual_out = made()
         ldro = _check_operand(residual_out, "residual_out", (M, H), dt, dev)
         r_ptr, g_ptr, ro_ptr = residual.data_ptr(), gamma.data_ptr(), residual_out.data_ptr()
     s = stream if stream is not None else torch.cuda.current_stream(dev)

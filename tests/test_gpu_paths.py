@@ -733,3 +733,38 @@ def test_pdl_codes_in_graph(ws, code):
     st = arf.arf_run_ex(ws.handle, bad, RMS, 8, ptrs.data_ptr(), R.data_ptr(), G.data_ptr(), 1e-6, out.data_ptr(),
                         ro.data_ptr(), 4, 7168, arf.ARF_BF16, torch.cuda.current_stream().cuda_stream)
     assert st == arf.ARF_ERR_INVALID_ARG
+
+
+def test_outputs_on_another_stream_are_not_memory_in_use(ws):
+    """run(stream=s) makes its outputs in that stream's memory: work queued on
+    the current stream may still read what was freed there."""
+    W, M, H = 2, 64, 1024
+    P = [torch.full((M, H), float(r + 1), dtype=torch.bfloat16, device="cuda:0") for r in range(W)]
+    R, G = torch.ones_like(P[0]), torch.ones(H, dtype=torch.bfloat16, device="cuda:0")
+    ptrs = arf.pointer_array(P)
+    want, want_ro = arf.run(ws, "rmsnorm", P, R, G, 1e-6, ptrs=ptrs)
+    s = torch.cuda.Stream()
+    arf.run(ws, "rmsnorm", P, R, G, 1e-6, ptrs=ptrs, stream=s)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    temps = [torch.full((M, H), 91.0, dtype=torch.bfloat16, device="cuda:0") for _ in range(4)]
+    kept = [torch.empty_like(x) for x in temps]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    for x, y in zip(temps, kept):
+        y.copy_(x)
+    freed = {x.data_ptr() for x in temps}
+    del temps, x
+    got = [arf.run(ws, "rmsnorm", P, R, G, 1e-6, ptrs=ptrs, stream=s) for _ in range(4)]
+    busy = not torch.cuda.current_stream().query()
+    again = {torch.empty_like(R).data_ptr() for _ in range(1)}
+    torch.cuda.synchronize()
+    assert busy, "the calls were made after the work on the current stream had ended"
+    assert freed & again, "nothing that was freed could have been handed out"
+    assert not freed & {t.data_ptr() for g in got for t in g}
+    for y in kept:
+        assert bool((y == 91.0).all())
+    for out, ro in got:
+        assert torch.equal(out, want) and torch.equal(ro, want_ro)
+    assert {seg["stream"] for seg in torch.cuda.memory_snapshot() for t in got[0]
+            if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]} == {s.cuda_stream}
