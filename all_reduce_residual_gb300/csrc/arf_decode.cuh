@@ -686,18 +686,21 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
                 qs[n][0] = qs[n][1] = p.score;
                 if constexpr (ES == 1) {
                     // q enters an fp16 product: times a power of two that
-                    // brings the head's largest value to [2^13, 2^14), which
-                    // is exact for what is within 2^-28 of it
+                    // brings the head's largest finite value to [2^13, 2^14),
+                    // which is exact for what is within 2^-28 of it (beside an
+                    // infinity too: one that a large value became would meet
+                    // it with either sign)
+                    const auto size = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.0f; };
                     float big = 0.0f;
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
                         const float2 x = MmaType<T>::unpack(qf[n][ks][0]), y = MmaType<T>::unpack(qf[n][ks][1]);
-                        big = fmaxf(big, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
+                        big = fmaxf(big, fmaxf(fmaxf(size(x.x), size(x.y)), fmaxf(size(y.x), size(y.y))));
                     }
                     big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
                     big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
                     int e = (int)(__float_as_uint(big) >> 23) - 127 - 13;  // floor(log2) - 13
-                    if (big == 0.0f || isinf(big)) e = 0;
+                    if (big == 0.0f) e = 0;
                     // 2^-e in two factors: each is a normal number
                     const float f0 = __uint_as_float((uint32_t)(127 - e / 2) << 23);
                     const float f1 = __uint_as_float((uint32_t)(127 - (e - e / 2)) << 23);

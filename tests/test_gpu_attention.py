@@ -1021,3 +1021,30 @@ def test_memory_in_use_elsewhere_is_not_written(ws):
         assert bool((y == 91).all())
     for g in got:
         ref.assert_decode(g, want, BF16)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_decode_infinite_queries_on_an_e4m3_cache(ws, dtype):
+    """A query with an infinity beside large finite values: scores of -inf are
+    masked out, and the finite values do not turn them into NaN."""
+    D, n, large = 64, 40, 1e30 if dtype == BF16 else 6e4
+    q = torch.zeros(1, 3, D, dtype=dtype)
+    q[..., 1], q[..., 2] = large, -large
+    q[0, 0, 0] = -math.inf    # every score is -inf
+    q[0, 1, 0] = math.inf     # +inf: the whole row is NaN
+    g = gen(3)
+    k = torch.zeros(3, 16, 1, D)
+    k[..., 0] = 1.0
+    k[..., 1:] = torch.randint(1, 5, (3, 16, 1, D - 1), generator=g).float()
+    v = torch.randn(3, 16, 1, D, generator=g)
+    kd, vd = k.to(E4M3), v.to(E4M3)
+    table, lens = torch.arange(3, dtype=torch.int32)[None], torch.tensor([n], dtype=torch.int32)
+    args = (table.to(DEV), lens.to(DEV))
+    out, lse = (x.cpu() for x in arf.paged_decode(ws, q.to(DEV), arf.KVCache(kd.to(DEV), vd.to(DEV)), *args,
+                                                  scale=1.0 / large))
+    assert not out[0, 0].any() and lse[0, 0] == -math.inf
+    assert bool(out[0, 1].isnan().all())
+    q[0, :2] = q[0, 2]
+    want = ref.decode(q, kd, vd, "nhd", table, lens, 1.0 / large)
+    ref.assert_close(out[0, 2], want[0][0, 2], want[2][0, 2] + ref.half_step(want[0][0, 2], dtype))
+    ref.assert_close(lse[0, 2], want[1][0, 2], want[3][0, 2])
