@@ -757,7 +757,8 @@ def test_outputs_on_another_stream_are_not_memory_in_use(ws):
     del temps, x
     got = [arf.run(ws, "rmsnorm", P, R, G, 1e-6, ptrs=ptrs, stream=s) for _ in range(4)]
     busy = not torch.cuda.current_stream().query()
-    again = {torch.empty_like(R).data_ptr() for _ in range(1)}
+    here = [torch.empty_like(R) for _ in range(8)]  # as many outputs on the current stream
+    again = {x.data_ptr() for x in here}
     torch.cuda.synchronize()
     assert busy, "the calls were made after the work on the current stream had ended"
     assert freed & again, "nothing that was freed could have been handed out"
