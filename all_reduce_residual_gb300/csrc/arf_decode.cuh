@@ -614,12 +614,9 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
     // caches, whose values can be infinite (a lower half of either sign or 0
     // would turn an infinite sum into NaN); e4m3 has no infinity
     constexpr int LO = ES == 2 ? 1 : 0;
-    // P as the sum of two 16-bit values where one alone would be as large an
-    // error as the rounding of out: bf16 (2^-9) for bf16, fp16 (2^-12) for
-    // fp16. For bf16 out of an fp16 product one value's error is an eighth of
-    // that rounding, and one is enough.
-    constexpr bool TWO = std::is_same<T, C>::value;
-    float o[1 + LO][NT][KS][4];
+    // P as the sum of two 16-bit values (2^-16 of it, or 2^-22 in fp16): one
+    // alone would be as large an error as the rounding of out for values of
+    // the cache's type, and an eighth of it for bf16 out of an fp16 product.
     // The softmax's reference, in units of log2, per head: kRoom below the
     // maximum when it was last set. It is set anew only when a score exceeds
     // it by more than `over` (kRoom + kSlack; -inf until the first score that
@@ -817,7 +814,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
                         }
                     }
             }
-            uint32_t ph[NT][MT][2], pl[NT][TWO ? MT : 1][2];
+            uint32_t ph[NT][MT][2], pl[NT][MT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -829,11 +826,9 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
                     const uint32_t h0 = MmaType<C>::pack(p0, p1), h1 = MmaType<C>::pack(p2, p3);
                     ph[n][i][0] = transpose8(h0);
                     ph[n][i][1] = transpose8(h1);
-                    if constexpr (TWO) {
-                        const float2 u0 = MmaType<C>::unpack(h0), u1 = MmaType<C>::unpack(h1);
-                        pl[n][i][0] = transpose8(MmaType<C>::pack(p0 - u0.x, p1 - u0.y));
-                        pl[n][i][1] = transpose8(MmaType<C>::pack(p2 - u1.x, p3 - u1.y));
-                    }
+                    const float2 u0 = MmaType<C>::unpack(h0), u1 = MmaType<C>::unpack(h1);
+                    pl[n][i][0] = transpose8(MmaType<C>::pack(p0 - u0.x, p1 - u0.y));
+                    pl[n][i][1] = transpose8(MmaType<C>::pack(p2 - u1.x, p3 - u1.y));
                 }
             // O^T += V^T P^T
 #pragma unroll
@@ -862,7 +857,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
                                 MmaType<C>::mma(o[0][n][c + half], x, ph[n][i][0], ph[n][i][1]);
-                                if constexpr (TWO) MmaType<C>::mma(o[0][n][c + half], x, pl[n][i][0], pl[n][i][1]);
+                                MmaType<C>::mma(o[0][n][c + half], x, pl[n][i][0], pl[n][i][1]);
                             }
                         }
                     }

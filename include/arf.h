@@ -581,8 +581,7 @@ arf_status_t arf_rotary_append(arf_workspace_t ws, const arf_rotary_t* rot, cons
  *   lse = m + ln sum_j exp(s_j - m),  m = max_j s_j
  * Scores, statistics and sums are binary32; the probabilities enter the
  * matrix instruction as the sum of two 16-bit values (a relative error of at
- * most 2^-16; bf16 queries on an e4m3 cache: as one fp16 value, 2^-11), out is
- * rounded once. A sequence without tokens (lens[b] <= 0
+ * most 2^-16), out is rounded once. A sequence without tokens (lens[b] <= 0
  * or every score -inf) gives out = 0 and lse = -inf.
  *   q, out       [B, heads, D], q->token_stride the stride of sequences;
  *                D in {64, 128, 256}; heads a multiple of kv_heads

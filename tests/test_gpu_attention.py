@@ -1013,7 +1013,8 @@ def test_memory_in_use_elsewhere_is_not_written(ws):
     del temps, x
     got = [arf.paged_decode(ws, q, cache, table, n, stream=s) for _ in range(8)]
     busy = not torch.cuda.current_stream().query()
-    again = [torch.empty(x, dtype=torch.uint8, device=DEV).data_ptr() for x in sizes]
+    here = [torch.empty(x, dtype=torch.uint8, device=DEV) for x in sizes for _ in range(4)]
+    again = [x.data_ptr() for x in here]
     torch.cuda.synchronize()
     assert busy, "the calls were made after the work on the current stream had ended"
     assert freed & set(again), "nothing that was freed could have been handed out"
@@ -1048,3 +1049,28 @@ def test_decode_infinite_queries_on_an_e4m3_cache(ws, dtype):
     want = ref.decode(q, kd, vd, "nhd", table, lens, 1.0 / large)
     ref.assert_close(out[0, 2], want[0][0, 2], want[2][0, 2] + ref.half_step(want[0][0, 2], dtype))
     ref.assert_close(lse[0, 2], want[1][0, 2], want[3][0, 2])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("width", [1, 4000])
+def test_decode_probabilities_on_an_e4m3_cache(ws, D, width):
+    """Values whose weighted sum cancels: what is left shows the rounding of
+    the probabilities, which out's own does not hide. They enter the product
+    as two fp16 values, off by 2^-16 of sum p |v| / sum p, for bf16 queries
+    too. Small queries keep the bound on the scores' own error below that."""
+    B, n, page = 64, 2, 16
+    g = gen(D)
+    q = (torch.randn(B, 1, D, generator=g) / D).to(BF16)
+    k = torch.randn(B, page, 1, D, generator=g).to(E4M3)
+    v = torch.empty(B, page, 1, D)
+    table = torch.full((B, width), -1, dtype=torch.int32)
+    table[:, 0] = torch.arange(B)
+    lens = torch.full((B,), n, dtype=torch.int32)
+    # both weights are near a half: the values +1, -1 leave their difference
+    v[:, 0::2], v[:, 1::2] = 1.0, -1.0
+    v = v.to(E4M3)
+    got = arf.paged_decode(ws, q.to(DEV), arf.KVCache(k.to(DEV), v.to(DEV)), table.to(DEV), lens.to(DEV))
+    out, lse, tol, ltol = ref.decode(q, k, v, "nhd", table[:, :1], lens, D ** -0.5)
+    # sum p |v| / sum p is 1 here; ref's bound holds 2^-11 of it
+    ref.assert_close(got[0], out, tol - 2.0 ** -11 + 2.0 ** -16 + ref.half_step(out, BF16), "out")
+    ref.assert_close(got[1], lse, ltol, "lse")
