@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
             const int2 r = token_range(p, len);
             if (threadIdx.x == 0 && (len < 0 || len > p.cap_tokens)) atomicAdd(p.bad, 1u);
             if (r.y > r.x) continue;
-            for (int x = threadIdx.x; x < p.heads * (D / 4); x += kDecThreads)
-                write_out<T>(p, e, x / (D / 4), x % (D / 4) * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f);
+            for (int64_t x = threadIdx.x; x < (int64_t)p.heads * (D / 4); x += kDecThreads)
+                write_out<T>(p, e, (int)(x / (D / 4)), (int)(x % (D / 4)) * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f);
         }
     };
     int first_b, first_off;  // first sequence, and the units of its items before ours

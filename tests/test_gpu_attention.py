@@ -1074,3 +1074,22 @@ def test_decode_probabilities_on_an_e4m3_cache(ws, D, width):
     # sum p |v| / sum p is 1 here; ref's bound holds 2^-11 of it
     ref.assert_close(got[0], out, tol - 2.0 ** -11 + 2.0 ** -16 + ref.half_step(out, BF16), "out")
     ref.assert_close(got[1], lse, ltol, "lse")
+
+
+def test_decode_more_heads_than_32_bits_of_chunks(ws):
+    """Heads times their 8-byte chunks beyond 2^31: a sequence without tokens
+    is answered in every head, one with a token too."""
+    D, heads, page = 256, (1 << 25) + 8, 16
+    kp, vp = (torch.randn(1, page, 1, D, generator=gen(i)).to(BF16).to(DEV) for i in (1, 2))
+    q = torch.ones(1, 1, D, dtype=BF16, device=DEV).expand(-1, heads, -1)
+    out = torch.full((1, heads, D), 3.0, dtype=BF16, device=DEV)
+    lse = torch.zeros(1, heads, device=DEV)
+    table = torch.zeros(1, 40, dtype=torch.int32, device=DEV)
+    cache, size = arf.KVCache(kp, vp), ctypes.c_size_t()
+    assert arf.arf_paged_decode_scratch_bytes(ws.handle, cache.struct, 1, heads, 40, 0, size) == arf.ARF_OK
+    assert size.value > 0, "the dealt form is meant"
+    lens = torch.zeros(1, dtype=torch.int32, device=DEV)
+    arf.paged_decode(ws, q, cache, table, lens, out=out, lse=lse)
+    assert bool((lse == -math.inf).all()) and not out.any()
+    arf.paged_decode(ws, q, cache, table, lens + 1, out=out, lse=lse)
+    assert bool((out == vp[0, 0]).all()) and bool((lse == lse[0, 0]).all())
