@@ -617,6 +617,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
     // P as the sum of two 16-bit values (2^-16 of it, or 2^-22 in fp16): one
     // alone would be as large an error as the rounding of out for values of
     // the cache's type, and an eighth of it for bf16 out of an fp16 product.
+    float o[1 + LO][NT][KS][4];
     // The softmax's reference, in units of log2, per head: kRoom below the
     // maximum when it was last set. It is set anew only when a score exceeds
     // it by more than `over` (kRoom + kSlack; -inf until the first score that
