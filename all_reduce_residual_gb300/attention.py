@@ -33,7 +33,7 @@ _SCALING = {None: B.ARF_ROPE_NONE, "none": B.ARF_ROPE_NONE, "linear": B.ARF_ROPE
 
 if not os.path.exists(os.path.join(B.PKG, "_torch_ops.so")):
     raise RuntimeError(f"{B.PKG}/_torch_ops.so is not built: run `python -m all_reduce_residual_gb300.build` "
-                       "(or __graft_entry__.build()); there is no other implementation")
+                       "(or __graft_entry__.build()) where torch is installed; there is no other implementation")
 B.load()  # the library itself, before the module that links against it
 from . import _torch_ops  # noqa: E402
 

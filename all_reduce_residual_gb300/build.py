@@ -4,11 +4,12 @@ the module _torch_ops that calls it on torch tensors.
 Each translation unit under csrc/ is compiled by nvcc (torch_ops.cpp by the
 host compiler against torch's headers) in parallel, then the objects are
 linked into a shared library next to this file with the CUDA runtime linked
-statically, and the module beside it. Built in place; the outputs are
-git-ignored.
+statically, and the module beside it. The library needs no torch: where there
+is none, it is built alone. Built in place; the outputs are git-ignored.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -41,6 +42,10 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libarf.so")
 
 
+def _has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def _torch_commands(obj: str, out: str):
     """The commands that compile and link the module against torch."""
     import torch
@@ -59,21 +64,35 @@ def _torch_commands(obj: str, out: str):
     return compile_cmd, link_cmd
 
 
-def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "arf.h"), __file__]
-    return [f for f in files if os.path.isfile(f)]
+def _newer(files, out) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(f) > os.path.getmtime(out) for f in files)
+
+
+def _lib_stale() -> bool:
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != TORCH_SOURCE]
+    return _newer([f for f in files if os.path.isfile(f)] + [os.path.join(INCLUDE, "arf.h"), __file__], LIB)
+
+
+def _module_stale() -> bool:
+    return _newer([os.path.join(CSRC, TORCH_SOURCE), os.path.join(INCLUDE, "arf.h"), __file__], TORCH_LIB)
 
 
 def stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(TORCH_LIB)):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return _lib_stale() or (_has_torch() and _module_stale())
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libarf.so and _torch_ops.so if they are missing or out of date."""
-    if not (force or stale()):
+    """Compile and link libarf.so and, where torch is installed, _torch_ops.so
+    if they are missing or out of date."""
+    lib, module = force or _lib_stale(), _has_torch() and (force or _module_stale())
+    if not (lib or module):
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
@@ -84,36 +103,27 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         cmd = [cc, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        said = _run(cmd, f"nvcc failed on {src}")
         if ptxas_info or verbose:
-            sys.stderr.write(r.stdout + r.stderr)
+            sys.stderr.write(said)
         return obj
 
-    torch_obj = os.path.join(BUILD_DIR, "torch_ops.o")
     torch_tmp = TORCH_LIB + ".tmp"
-    torch_compile, torch_link = _torch_commands(torch_obj, torch_tmp)
-
-    def compile_torch():
-        r = subprocess.run(torch_compile, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{torch_compile[0]} failed on {TORCH_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    if module:
+        torch_compile, torch_link = _torch_commands(os.path.join(BUILD_DIR, "torch_ops.o"), torch_tmp)
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        torch_done = ex.submit(compile_torch)
-        objs = list(ex.map(compile_one, SOURCES))
-        torch_done.result()
-    tmp = LIB + ".tmp"
-    cmd = [cc, GENCODE, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    r = subprocess.run(torch_link, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of _torch_ops failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(torch_tmp, TORCH_LIB)
+        torch_done = ex.submit(_run, torch_compile, f"compiler failed on {TORCH_SOURCE}") if module else None
+        objs = list(ex.map(compile_one, SOURCES)) if lib else []
+        if lib:
+            tmp = LIB + ".tmp"
+            _run([cc, GENCODE, "-shared", "-cudart", "static", "-o", tmp, *objs], "link failed")
+            os.replace(tmp, LIB)
+        if module:
+            torch_done.result()
+    if module:
+        _run(torch_link, "link of _torch_ops failed")
+        os.replace(torch_tmp, TORCH_LIB)
     return LIB
 
 
