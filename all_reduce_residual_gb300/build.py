@@ -25,6 +25,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libarf.so")
 TORCH_SOURCE = "torch_ops.cpp"
 TORCH_LIB = os.path.join(PKG, "_torch_ops.so")
+TORCH_STAMP = os.path.join(BUILD_DIR, "torch_ops.stamp")  # what the module was built against
 
 SOURCES = ["arf_api.cu", "arf_launch_bf16.cu", "arf_launch_fp16.cu", "arf_static.cu", "arf_measure.cu",
            "arf_rotary.cu", "arf_decode.cu", "arf_decode_bf16.cu", "arf_decode_fp16.cu", "arf_pages.cu"]
@@ -42,8 +43,15 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libarf.so")
 
 
-def _has_torch() -> bool:
-    return importlib.util.find_spec("torch") is not None
+def _torch_stamp():
+    """The interpreter and the torch that the module is bound to (by torch's
+    C++ layout), or None without torch. Does not import torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    root = os.path.dirname(spec.origin)
+    with open(os.path.join(root, "version.py")) as f:
+        return "\n".join((sys.version, root, f.read()))
 
 
 def _torch_commands(obj: str, out: str):
@@ -73,12 +81,19 @@ def _lib_stale() -> bool:
     return _newer([f for f in files if os.path.isfile(f)] + [os.path.join(INCLUDE, "arf.h"), __file__], LIB)
 
 
-def _module_stale() -> bool:
-    return _newer([os.path.join(CSRC, TORCH_SOURCE), os.path.join(INCLUDE, "arf.h"), __file__], TORCH_LIB)
+def _module_stale(stamp) -> bool:
+    if stamp is None:
+        return False
+    if _newer([os.path.join(CSRC, TORCH_SOURCE), os.path.join(INCLUDE, "arf.h"), __file__], TORCH_LIB):
+        return True
+    if not os.path.exists(TORCH_STAMP):
+        return True
+    with open(TORCH_STAMP) as f:
+        return f.read() != stamp
 
 
 def stale() -> bool:
-    return _lib_stale() or (_has_torch() and _module_stale())
+    return _lib_stale() or _module_stale(_torch_stamp())
 
 
 def _run(cmd, what):
@@ -91,7 +106,8 @@ def _run(cmd, what):
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link libarf.so and, where torch is installed, _torch_ops.so
     if they are missing or out of date."""
-    lib, module = force or _lib_stale(), _has_torch() and (force or _module_stale())
+    stamp = _torch_stamp()
+    lib, module = force or _lib_stale(), stamp is not None and (force or _module_stale(stamp))
     if not (lib or module):
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -124,6 +140,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if module:
         _run(torch_link, "link of _torch_ops failed")
         os.replace(torch_tmp, TORCH_LIB)
+        with open(TORCH_STAMP, "w") as f:
+            f.write(stamp)
     return LIB
 
 
