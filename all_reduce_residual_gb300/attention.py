@@ -16,7 +16,9 @@ elsewhere still uses them; the caller orders what the call reads, and what
 later reads its outputs, as between any two streams. Nothing is read
 back, so they can be captured into CUDA graphs. The checks and the call itself
 are in the module _torch_ops (csrc/torch_ops.cpp), for the host's time. No
-gradients are recorded.
+gradients are recorded: a tensor that requires one is refused unless gradients
+are off (torch.no_grad, torch.inference_mode), and tensors that a call writes
+count as modified in place.
 """
 from __future__ import annotations
 
@@ -101,8 +103,8 @@ class KVCache:
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, d
         self.struct = B.Cache(k.data_ptr(), v.data_ptr(), pages, page_size, heads, d, sp, st, sh,
                               _CACHE_DTYPE[k.dtype], k_scale, v_scale)
-        # what _torch_ops reads: the struct's address, and the device
-        self._cache_key = (ctypes.addressof(self.struct), k.get_device())
+        # what _torch_ops reads: the struct's address, the device, the tensors
+        self._cache_key = (ctypes.addressof(self.struct), k.get_device(), k, v)
 
 
 def rotary(ws, q, k, positions, table: RotaryTable, q_out=None, k_out=None, stream=None):

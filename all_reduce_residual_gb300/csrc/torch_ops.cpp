@@ -10,6 +10,7 @@
 // them the launch), 3.6 with outputs made.
 #include <ATen/core/Tensor.h>
 #include <c10/core/Allocator.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/StorageImpl.h>
 #include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -61,6 +62,20 @@ void on_device(const Tensor& t, const char* name, int device) {
     TORCH_CHECK_VALUE(t.is_cuda() && t.get_device() == device, name, " is on ", t.device(), ", expected cuda:", device);
 }
 
+// These calls record no gradients: a tensor that wants one is refused rather
+// than left out of it without a word.
+void no_gradient(const Tensor& t, const char* name) {
+    TORCH_CHECK_VALUE(!t.requires_grad() || !c10::GradMode::is_enabled(), name,
+                      " requires a gradient, which this call does not record: detach it, or call under torch.no_grad()");
+}
+// A given tensor was written: what autograd has saved of it is stale.
+void written(const Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject* o) {
+    if (!none(o)) written(THPVariable_Unpack(o));
+}
+
 // t [rows, heads, D]; sizes below 0 are free.
 arf_heads_t heads(const Tensor& t, const char* name, ScalarType dtype, int device, int64_t rows = -1, int64_t n = -1,
                   int64_t D = -1) {
@@ -69,6 +84,7 @@ arf_heads_t heads(const Tensor& t, const char* name, ScalarType dtype, int devic
                       name, ": shape ", t.sizes(), ", expected [rows, heads, D] that fit the other arguments");
     TORCH_CHECK_VALUE(t.scalar_type() == dtype, name, ": dtype ", t.scalar_type(), " != ", dtype);
     on_device(t, name, device);
+    no_gradient(t, name);
     TORCH_CHECK_VALUE(t.stride(2) == 1 || t.size(2) <= 1, name, ": the elements of a head must be contiguous");
     TORCH_CHECK_VALUE(t.size(1) <= INT32_MAX, name, ": too many heads");
     return {t.data_ptr(), t.stride(0), t.stride(1), (int)t.size(1)};
@@ -154,30 +170,46 @@ Pair empty_pair(const Stream& stream, at::IntArrayRef size0, ScalarType dtype0, 
 }
 
 // The C struct behind a handle object of attention.py: its attribute `key`
-// is (address of the struct, device index).
+// is a tuple (address of the struct, device index, and the tensors of a cache:
+// keys, values).
 PyObject* kCacheKey = nullptr;  // the attributes' names, interned at import
 PyObject* kTableKey = nullptr;
 
-int64_t struct_of(PyObject* o, PyObject* key, const char* what, int device) {
-    PyObject* pair = PyObject_GetAttr(o, key);
-    if (!pair) {
+// The tuple (a borrowed reference: `o` holds it) and the struct's address.
+struct Handle {
+    PyObject* key;
+    int64_t at;
+};
+Handle handle_of(PyObject* o, PyObject* name, Py_ssize_t size, const char* what, int device) {
+    PyObject* key = PyObject_GetAttr(o, name);
+    if (!key) {
         PyErr_Clear();
         TORCH_CHECK_VALUE(false, "a ", what, " is required");
     }
-    const bool is_pair = PyTuple_Check(pair) && PyTuple_GET_SIZE(pair) == 2;
-    const int64_t at = is_pair ? PyLong_AsLongLong(PyTuple_GET_ITEM(pair, 0)) : 0;
-    const int64_t dev = is_pair ? PyLong_AsLongLong(PyTuple_GET_ITEM(pair, 1)) : -1;
-    Py_DECREF(pair);
+    Py_DECREF(key);
+    const bool fits = PyTuple_Check(key) && PyTuple_GET_SIZE(key) == size;
+    const int64_t at = fits ? PyLong_AsLongLong(PyTuple_GET_ITEM(key, 0)) : 0;
+    const int64_t dev = fits ? PyLong_AsLongLong(PyTuple_GET_ITEM(key, 1)) : -1;
     if (PyErr_Occurred()) throw python_error();
     TORCH_CHECK_VALUE(at != 0, "a ", what, " is required");
     TORCH_CHECK_VALUE(dev == device, "the ", what, " is on device ", dev, ", expected cuda:", device);
-    return at;
+    return {key, at};
 }
-const arf_kv_cache_t* cache_of(PyObject* o, int device) {
-    return reinterpret_cast<const arf_kv_cache_t*>(struct_of(o, kCacheKey, "KVCache", device));
+struct Cache {
+    const arf_kv_cache_t* c;
+    PyObject* key;
+    const Tensor& pages(int i) const { return THPVariable_Unpack(PyTuple_GET_ITEM(key, 2 + i)); }
+    void written_to() const { written(pages(0)), written(pages(1)); }
+    const arf_kv_cache_t* operator->() const { return c; }
+};
+Cache cache_of(PyObject* o, int device) {
+    const Handle h = handle_of(o, kCacheKey, 4, "KVCache", device);
+    const Cache cache = {reinterpret_cast<const arf_kv_cache_t*>(h.at), h.key};
+    for (int i = 0; i < 2; ++i) no_gradient(tensor(PyTuple_GET_ITEM(h.key, 2 + i), "the KVCache"), "the KVCache");
+    return cache;
 }
 const arf_rotary_t* rotary_of(PyObject* o, int device) {
-    return reinterpret_cast<const arf_rotary_t*>(struct_of(o, kTableKey, "RotaryTable", device));
+    return reinterpret_cast<const arf_rotary_t*>(handle_of(o, kTableKey, 2, "RotaryTable", device).at);
 }
 
 // A closed Workspace's handle is None: the library refuses a null workspace.
@@ -233,6 +265,8 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const arf_status_t r = arf_rotary(workspace(a[0]), table, static_cast<const int32_t*>(pos), T, (int)D, dt, &qh, &qo,
                                       has_k ? &kh : nullptr, has_k ? &ko : nullptr, stream.raw());
     if (r != ARF_OK) return status(r);
+    written(a[6]);
+    written(a[7]);
     PyObject* out = PyTuple_New(2);
     if (!out) throw python_error();
     PyObject* first = a[6];
@@ -254,7 +288,7 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& k = tensor(a[3], "k");
     const arf_dtype_t dt = io_dtype(k, "k");
     const ScalarType st = k.scalar_type();
-    const arf_kv_cache_t* cache = cache_of(a[8], device);
+    const Cache cache = cache_of(a[8], device);
     TORCH_CHECK_VALUE(k.dim() == 3, "k: shape ", k.sizes(), ", expected [rows, heads, D]");
     const int64_t T = k.size(0), D = cache->head_dim;
     const arf_heads_t kh = heads(k, "k", st, device, T, cache->kv_heads, D);
@@ -282,8 +316,10 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const arf_status_t r = arf_rotary_append(workspace(a[0]), table, static_cast<const int32_t*>(pos),
                                              static_cast<const int64_t*>(slots), T, dt, has_q ? &qh : nullptr,
-                                             has_q ? &qo : nullptr, &kh, &vh, cache, stream.raw());
+                                             has_q ? &qo : nullptr, &kh, &vh, cache.c, stream.raw());
     if (r != ARF_OK) return status(r);
+    written(a[9]);
+    cache.written_to();
     if (q_out.defined()) return THPVariable_Wrap(std::move(q_out));
     PyObject* out = has_q ? a[9] : Py_None;
     Py_INCREF(out);
@@ -300,7 +336,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& q = tensor(a[2], "q");
     const arf_dtype_t dt = io_dtype(q, "q");
     const ScalarType st = q.scalar_type();
-    const arf_kv_cache_t* cache = cache_of(a[3], device);
+    const Cache cache = cache_of(a[3], device);
     const arf_heads_t qh = heads(q, "q", st, device);
     const int64_t B = q.size(0), D = q.size(2);
     TORCH_CHECK_VALUE(D == cache->head_dim && cache->kv_heads > 0 && qh.heads % cache->kv_heads == 0, "q: ", qh.heads,
@@ -342,6 +378,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                               l.size(1) == qh.heads && l.is_contiguous(),
                           "lse: contiguous float32 [", B, ", ", qh.heads, "] expected");
         on_device(l, "lse", device);
+        no_gradient(l, "lse");
         lse_ptr = static_cast<float*>(l.data_ptr());
     }
     // scratch of the caching allocator (512-byte aligned), from the pool of
@@ -349,15 +386,17 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     // memory, work on other streams may not
     size_t bytes = 0;
     const arf_status_t need =
-        arf_paged_decode_scratch_bytes(workspace(a[0]), cache, B, qh.heads, (int32_t)width, window, &bytes);
+        arf_paged_decode_scratch_bytes(workspace(a[0]), cache.c, B, qh.heads, (int32_t)width, window, &bytes);
     if (need != ARF_OK) return status(need);
     Tensor scratch;
     if (bytes > 0) scratch = empty(stream, {(int64_t)bytes}, ScalarType::Byte);
     const arf_status_t r =
-        arf_paged_decode(workspace(a[0]), cache, B, dt, &qh, static_cast<const int32_t*>(table.data_ptr()),
+        arf_paged_decode(workspace(a[0]), cache.c, B, dt, &qh, static_cast<const int32_t*>(table.data_ptr()),
                          B > 1 ? table.stride(0) : width, (int32_t)width, static_cast<const int32_t*>(lens), scale, cap,
                          window, &oh, lse_ptr, bytes > 0 ? scratch.data_ptr() : nullptr, bytes, stream.raw());
     if (r != ARF_OK) return status(r);
+    written(a[9]);
+    written(a[10]);
     PyObject* pair = PyTuple_New(2);
     if (!pair) throw python_error();
     PyObject* first = a[9];
@@ -403,17 +442,25 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int device = (int)integer(a[1]);
     TORCH_CHECK_VALUE(PyList_Check(a[2]) || PyTuple_Check(a[2]), "caches: a list or a tuple");
     std::vector<arf_kv_cache_t> caches;
+    std::vector<Cache> handles;
     const Py_ssize_t count = PySequence_Fast_GET_SIZE(a[2]);
     TORCH_CHECK_VALUE(count > 0, "at least one cache is required");
     TORCH_CHECK_VALUE(count <= INT32_MAX, "too many caches");
     caches.reserve((size_t)count);
-    for (Py_ssize_t i = 0; i < count; ++i) caches.push_back(*cache_of(PySequence_Fast_GET_ITEM(a[2], i), device));
+    handles.reserve((size_t)count);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        handles.push_back(cache_of(PySequence_Fast_GET_ITEM(a[2], i), device));
+        caches.push_back(*handles.back().c);
+    }
     const std::vector<int32_t> src = page_numbers(a[3], "src"), dst = page_numbers(a[4], "dst");
     TORCH_CHECK_VALUE(src.size() == dst.size(), src.size(), " sources and ", dst.size(), " destinations");
     TORCH_CHECK_VALUE(src.size() <= INT32_MAX, "too many pages");
     const Stream stream(a[5], device);
-    return status(arf_copy_pages(workspace(a[0]), caches.data(), (int)count, src.data(), dst.data(), (int)src.size(),
-                                 stream.raw()));
+    const arf_status_t r = arf_copy_pages(workspace(a[0]), caches.data(), (int)count, src.data(), dst.data(),
+                                          (int)src.size(), stream.raw());
+    if (r == ARF_OK)
+        for (const Cache& cache : handles) cache.written_to();
+    return status(r);
     END_HANDLE_TH_ERRORS
 }
 

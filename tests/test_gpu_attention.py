@@ -1093,3 +1093,63 @@ def test_decode_more_heads_than_32_bits_of_chunks(ws):
     assert bool((lse == -math.inf).all()) and not out.any()
     arf.paged_decode(ws, q, cache, table, lens + 1, out=out, lse=lse)
     assert bool((out == vp[0, 0]).all()) and bool((lse == lse[0, 0]).all())
+
+
+# ---- autograd --------------------------------------------------------------------
+
+
+def test_gradients_are_refused(ws):
+    q, k = (randn((2, h, 64), BF16, h).to(DEV) for h in (4, 2))
+    pos = torch.zeros(2, dtype=torch.int32, device=DEV)
+    kp, vp = (torch.zeros(2, 16, 2, 64, dtype=BF16, device=DEV) for _ in range(2))
+    cache, rot, table = arf.KVCache(kp, vp), arf.RotaryTable(64), pos[:, None].contiguous()
+    grad = lambda x: x.clone().requires_grad_()  # noqa: E731
+    lse = torch.zeros(2, 4, device=DEV)
+    calls = [lambda: arf.rotary(ws, grad(q), k, pos, rot), lambda: arf.rotary(ws, q, grad(k), pos, rot),
+             lambda: arf.rotary(ws, q, k, pos, rot, q_out=grad(q)), lambda: arf.rotary(ws, q * grad(q), None, pos, rot),
+             lambda: arf.rotary_append(ws, q, k, grad(k), pos, pos.long(), rot, cache),
+             lambda: arf.rotary_append(ws, q, grad(k), k, pos, pos.long(), rot, cache),
+             lambda: arf.rotary_append(ws, q, k, k, pos, pos.long(), rot, arf.KVCache(kp, grad(vp))),
+             lambda: arf.paged_decode(ws, grad(q), cache, table, pos), lambda: arf.paged_decode(ws, q, cache, table, pos, lse=grad(lse)),
+             lambda: arf.paged_decode(ws, q, cache, table, pos, out=grad(q)),
+             lambda: arf.paged_decode(ws, q, arf.KVCache(grad(kp), vp), table, pos),
+             lambda: arf.copy_pages(ws, [cache, arf.KVCache(kp, grad(vp))], [0], [1])]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    for off in (torch.no_grad, torch.inference_mode):
+        with off():
+            for call in calls:
+                call()
+
+
+def test_what_a_call_writes_counts_as_modified(ws):
+    """Autograd must not use what it saved of a tensor that a call has
+    overwritten."""
+    pos = torch.zeros(2, dtype=torch.int32, device=DEV)
+    rot = arf.RotaryTable(64)
+
+    def stale(x, call):
+        w = torch.ones((), dtype=x.dtype, device=DEV, requires_grad=True)
+        y = (w * x).sum()  # saves x
+        version = x._version
+        call()
+        assert x._version > version
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+
+    q, k = (randn((2, h, 64), BF16, h).to(DEV) for h in (4, 2))
+    stale(q, lambda: arf.rotary(ws, q, None, pos, rot, q_out=q))
+    stale(k, lambda: arf.rotary(ws, q, k, pos, rot, k_out=k))
+    for i in range(2):
+        pages_ = [torch.zeros(2, 16, 2, 64, dtype=BF16, device=DEV) for _ in range(2)]
+        cache = arf.KVCache(*pages_)
+        stale(pages_[i], lambda: arf.rotary_append(ws, None, k, k, None, pos.long(), None, cache))
+        stale(pages_[i], lambda: arf.copy_pages(ws, [cache], [0], [1]))
+    out, lse = torch.zeros_like(q), torch.zeros(2, 4, device=DEV)
+    stale(out, lambda: arf.paged_decode(ws, q, cache, pos[:, None], pos, out=out))
+    stale(lse, lambda: arf.paged_decode(ws, q, cache, pos[:, None], pos, lse=lse))
+    stale(out, lambda: arf.rotary_append(ws, q, k, k, pos, pos.long(), rot, cache, q_out=out))
+    with torch.inference_mode():  # has no versions
+        x = torch.zeros_like(q)
+        arf.rotary(ws, q, None, pos, rot, q_out=x)
