@@ -44,6 +44,10 @@ def _raise(ws, st, what):
     raise B.ArfError(st, what, B.arf_last_cuda_error(ws.handle) if st == B.ARF_ERR_CUDA else 0)
 
 
+def _fixed(name):
+    return property(lambda self: getattr(self, "_" + name))
+
+
 class RotaryTable:
     """The angles per position of a model's rotary positions, on the device
     (arf_rotary_turns); made once and kept.
@@ -67,14 +71,17 @@ class RotaryTable:
                                 turns, mag)
         if st != B.ARF_OK:
             raise B.ArfError(st, "arf_rotary_turns")
-        self.rot_dim, self.layout, self.magnitude = rot_dim, layout, mag.value
+        self._rot_dim, self._layout, self._magnitude = rot_dim, layout, mag.value
         # torch has no 64-bit unsigned type that kernels need here: the same bits as int64
         host = torch.frombuffer(turns, dtype=torch.int64)
-        self.turns = host.clone() if device is not None and torch.device(device).type == "cpu" else \
+        self._turns = host.clone() if device is not None and torch.device(device).type == "cpu" else \
             host.to(device if device is not None else torch.device("cuda", torch.cuda.current_device()))
-        self.struct = B.Rotary(self.turns.data_ptr(), rot_dim, int(layout == "interleaved"), mag.value)
+        self._struct = B.Rotary(self._turns.data_ptr(), rot_dim, int(layout == "interleaved"), mag.value)
         # what _torch_ops reads: the struct's address, and the device
-        self._table_key = (ctypes.addressof(self.struct), self.turns.get_device())
+        self._table_key = (ctypes.addressof(self._struct), self._turns.get_device())
+
+    # the struct holds the table's address: a table is made anew, not changed
+    rot_dim, layout, magnitude, turns, struct = map(_fixed, ("rot_dim", "layout", "magnitude", "turns", "struct"))
 
 
 class KVCache:
@@ -99,12 +106,17 @@ class KVCache:
         pages, a, b, d = k.shape
         sp, sa, sb, _ = k.stride()
         (page_size, heads), (st, sh) = ((a, b), (sa, sb)) if layout == "nhd" else ((b, a), (sb, sa))
-        self.k, self.v, self.layout, self.dtype, self.device = k, v, layout, k.dtype, k.device
-        self.num_pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, d
-        self.struct = B.Cache(k.data_ptr(), v.data_ptr(), pages, page_size, heads, d, sp, st, sh,
+        self._k, self._v, self._layout = k, v, layout
+        self._num_pages, self._page_size, self._kv_heads, self._head_dim = pages, page_size, heads, d
+        self._struct = B.Cache(k.data_ptr(), v.data_ptr(), pages, page_size, heads, d, sp, st, sh,
                               _CACHE_DTYPE[k.dtype], k_scale, v_scale)
         # what _torch_ops reads: the struct's address, the device, the tensors
-        self._cache_key = (ctypes.addressof(self.struct), k.get_device(), k, v)
+        self._cache_key = (ctypes.addressof(self._struct), k.get_device(), k, v)
+
+    # the struct holds the pages' addresses: a cache of other pages is made anew
+    k, v, layout, num_pages, page_size, kv_heads, head_dim, struct = map(
+        _fixed, ("k", "v", "layout", "num_pages", "page_size", "kv_heads", "head_dim", "struct"))
+    dtype, device = property(lambda self: self._k.dtype), property(lambda self: self._k.device)
 
 
 def rotary(ws, q, k, positions, table: RotaryTable, q_out=None, k_out=None, stream=None):

@@ -385,3 +385,15 @@ def test_pool_from_several_threads():
         [t.join() for t in ts]
         assert pool.free_pages == 256
         assert np.array_equal(pool.pages(pool.open(12)), [0, 1, 2])
+
+
+def test_handles_do_not_change_under_their_structs():
+    """A table's struct holds an address: what it is made of is not replaced."""
+    t = arf.RotaryTable(8, device="cpu")
+    for name, value in (("turns", t.turns.clone()), ("rot_dim", 4), ("layout", "interleaved"), ("magnitude", 2.0),
+                        ("struct", None)):
+        with pytest.raises(AttributeError):
+            setattr(t, name, value)
+    assert t.struct.turns == t.turns.data_ptr() and t.struct.rot_dim == t.rot_dim
+    for name in ("k", "v", "layout", "dtype", "device", "num_pages", "page_size", "kv_heads", "head_dim", "struct"):
+        assert getattr(arf.KVCache, name).fset is None
