@@ -44,6 +44,31 @@ def _raise(ws, st, what):
     raise B.ArfError(st, what, B.arf_last_cuda_error(ws.handle) if st == B.ARF_ERR_CUDA else 0)
 
 
+def _share(delta, dims, row):
+    """Whether two tensors of rows of `row` bytes, at offsets sum(i * stride)
+    of 0 <= i < n for every (stride, n) of `dims`, have a byte in common when
+    the second begins `delta` bytes after the first. The rows of one do not
+    overlap (each stride is beyond all that is inside it); of other tensors
+    no library call writes."""
+    if any(n == 0 for _, n in dims):
+        return False
+    dims = sorted((d for d in dims if d[1] > 1), reverse=True)
+    reach = row - 1 + sum(stride * (n - 1) for stride, n in dims)  # the largest distance of two bytes
+
+    def meets(rest, reach, dims):
+        if abs(rest) > reach:
+            return False
+        if not dims:
+            return True
+        (stride, n), *inner = dims
+        if stride == 0:
+            return meets(rest, reach, inner)
+        return any(-n < i < n and meets(rest - i * stride, reach - stride * (n - 1), inner)
+                   for i in (rest // stride, rest // stride + 1))
+
+    return meets(delta, reach, dims)
+
+
 def _fixed(name):
     return property(lambda self: getattr(self, "_" + name))
 
@@ -89,7 +114,8 @@ class KVCache:
 
     k, v: [pages, page_size, kv_heads, D] (layout "nhd") or [pages, kv_heads,
     page_size, D] ("hnd"), of equal shape and strides, D contiguous; bf16,
-    fp16 or float8_e4m3fn (which holds value / scale).
+    fp16 or float8_e4m3fn (which holds value / scale). They may be views of one
+    tensor; a cache whose keys and values share elements can only be read.
     """
 
     def __init__(self, k, v, layout: str = "nhd", k_scale: float = 1.0, v_scale: float = 1.0):
@@ -110,8 +136,12 @@ class KVCache:
         self._num_pages, self._page_size, self._kv_heads, self._head_dim = pages, page_size, heads, d
         self._struct = B.Cache(k.data_ptr(), v.data_ptr(), pages, page_size, heads, d, sp, st, sh,
                               _CACHE_DTYPE[k.dtype], k_scale, v_scale)
-        # what _torch_ops reads: the struct's address, the device, the tensors
-        self._cache_key = (ctypes.addressof(self._struct), k.get_device(), k, v)
+        # keys and values that share memory can be read; a call that writes
+        # them would leave which of the two is there to chance
+        es = k.element_size()
+        shared = _share(v.data_ptr() - k.data_ptr(), [(sp * es, pages), (sa * es, a), (sb * es, b)], d * es)
+        # what _torch_ops reads: the struct's address, the device, the tensors, whether they may be written
+        self._cache_key = (ctypes.addressof(self._struct), k.get_device(), k, v, not shared)
 
     # the struct holds the pages' addresses: a cache of other pages is made anew
     k, v, layout, num_pages, page_size, kv_heads, head_dim, struct = map(

@@ -170,8 +170,8 @@ Pair empty_pair(const Stream& stream, at::IntArrayRef size0, ScalarType dtype0, 
 }
 
 // The C struct behind a handle object of attention.py: its attribute `key`
-// is a tuple (address of the struct, device index, and the tensors of a cache:
-// keys, values).
+// is a tuple (address of the struct, device index; of a cache also its keys,
+// its values, and whether they may be written).
 PyObject* kCacheKey = nullptr;  // the attributes' names, interned at import
 PyObject* kTableKey = nullptr;
 
@@ -199,11 +199,15 @@ struct Cache {
     const arf_kv_cache_t* c;
     PyObject* key;
     const Tensor& pages(int i) const { return THPVariable_Unpack(PyTuple_GET_ITEM(key, 2 + i)); }
+    void check_writable() const {
+        TORCH_CHECK_VALUE(PyTuple_GET_ITEM(key, 4) == Py_True,
+                          "the KVCache's keys and values share elements: it can only be read");
+    }
     void written_to() const { written(pages(0)), written(pages(1)); }
     const arf_kv_cache_t* operator->() const { return c; }
 };
 Cache cache_of(PyObject* o, int device) {
-    const Handle h = handle_of(o, kCacheKey, 4, "KVCache", device);
+    const Handle h = handle_of(o, kCacheKey, 5, "KVCache", device);
     const Cache cache = {reinterpret_cast<const arf_kv_cache_t*>(h.at), h.key};
     for (int i = 0; i < 2; ++i) no_gradient(tensor(PyTuple_GET_ITEM(h.key, 2 + i), "the KVCache"), "the KVCache");
     return cache;
@@ -289,6 +293,7 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const arf_dtype_t dt = io_dtype(k, "k");
     const ScalarType st = k.scalar_type();
     const Cache cache = cache_of(a[8], device);
+    cache.check_writable();
     TORCH_CHECK_VALUE(k.dim() == 3, "k: shape ", k.sizes(), ", expected [rows, heads, D]");
     const int64_t T = k.size(0), D = cache->head_dim;
     const arf_heads_t kh = heads(k, "k", st, device, T, cache->kv_heads, D);
@@ -450,6 +455,7 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     handles.reserve((size_t)count);
     for (Py_ssize_t i = 0; i < count; ++i) {
         handles.push_back(cache_of(PySequence_Fast_GET_ITEM(a[2], i), device));
+        handles.back().check_writable();
         caches.push_back(*handles.back().c);
     }
     const std::vector<int32_t> src = page_numbers(a[3], "src"), dst = page_numbers(a[4], "dst");

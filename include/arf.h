@@ -483,7 +483,9 @@ typedef struct arf_heads {
  * `v` alike. Row and head order inside a page are free (heads outermost or
  * tokens outermost). A 16-bit cache holds the values themselves. An e4m3
  * cache holds value / scale, rounded to nearest even and saturated to +-448
- * (NaN stays NaN); scales must be 1 for a 16-bit cache. */
+ * (NaN stays NaN); scales must be 1 for a 16-bit cache. What elements that k
+ * and v share hold after a call that writes the cache (arf_rotary_append,
+ * arf_copy_pages) is unspecified. */
 typedef struct arf_kv_cache {
     void* k;               /* device */
     void* v;               /* device */

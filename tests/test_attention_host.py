@@ -397,3 +397,24 @@ def test_handles_do_not_change_under_their_structs():
     assert t.struct.turns == t.turns.data_ptr() and t.struct.rot_dim == t.rot_dim
     for name in ("k", "v", "layout", "dtype", "device", "num_pages", "page_size", "kv_heads", "head_dim", "struct"):
         assert getattr(arf.KVCache, name).fset is None
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_shared_elements_are_found(seed):
+    """_share against the sets of bytes, for page tensors of every layout and
+    offsets around those at which they begin to touch."""
+    from all_reduce_residual_gb300.attention import _share
+    rng = random.Random(seed)
+    sizes = [rng.randint(1, 4) for _ in range(3)]
+    row, inside, dims = rng.randint(1, 5), 0, []
+    inside = row
+    for n in sizes:  # each step beyond everything inside it
+        stride = inside + rng.choice([0, 0, 1, rng.randint(0, 9)])
+        dims.append((stride, n))
+        inside += stride * (n - 1)
+    rng.shuffle(dims)
+    at = {sum(i * s for i, (s, _) in zip(index, dims)) + d
+          for index in np.ndindex(*[n for _, n in dims]) for d in range(row)}
+    for delta in range(-inside - 3, inside + 4):
+        assert _share(delta, dims, row) == bool(at & {x + delta for x in at}), (delta, dims, row)
+    assert not _share(0, [(8, 0), (4, 2), (2, 2)], 2)

@@ -1153,3 +1153,28 @@ def test_what_a_call_writes_counts_as_modified(ws):
     with torch.inference_mode():  # has no versions
         x = torch.zeros_like(q)
         arf.rotary(ws, q, None, pos, rot, q_out=x)
+
+
+def test_keys_and_values_that_share_elements(ws):
+    """They can be read, not written; views that only interleave can."""
+    page, H, D = 8, 2, 64
+    base = torch.randn(6, 2 * page, H, D, generator=gen(1)).to(BF16).to(DEV)
+    before = base.clone()
+    k = randn((3, H, D), BF16, 2).to(DEV)
+    slots = torch.arange(3, device=DEV)
+    q, table, lens = randn((1, 4, D), BF16, 3).to(DEV), torch.arange(3, dtype=torch.int32)[None], torch.tensor([20])
+    for a, b in ((base[:4, :page], base[:4, :page]), (base[:4, :page], base[1:5, :page]),
+                 (base[:4, :page], base[:4, 1:page + 1]), (base[:4, :page], base[1:5, page - 1:2 * page - 1])):
+        cache = arf.KVCache(a, b)
+        for call in (lambda: arf.rotary_append(ws, None, k, k, None, slots, None, cache),
+                     lambda: arf.copy_pages(ws, cache, [0], [1])):
+            with pytest.raises(ValueError, match="share"):
+                call()
+        got = arf.paged_decode(ws, q, cache, table.to(DEV), lens.int().to(DEV))
+        want = ref.decode(q.cpu(), a.cpu(), b.cpu(), "nhd", table, lens, D ** -0.5)
+        ref.assert_decode(got, want, BF16)
+    assert torch.equal(base, before)
+    cache = arf.KVCache(base[:, :page], base[:, page:])
+    arf.rotary_append(ws, None, k, k, None, slots, None, cache)
+    arf.copy_pages(ws, cache, [0], [1])
+    assert torch.equal(base[1], base[0]) and torch.equal(base[0, :3], k) and torch.equal(base[0, page:page + 3], k)
