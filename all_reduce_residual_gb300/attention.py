@@ -23,6 +23,7 @@ count as modified in place.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -42,6 +43,14 @@ from . import _torch_ops  # noqa: E402
 
 def _raise(ws, st, what):
     raise B.ArfError(st, what, B.arf_last_cuda_error(ws.handle) if st == B.ARF_ERR_CUDA else 0)
+
+
+def _int(x, bits, name):
+    """x as a signed C integer of so many bits (ctypes would cut it off)."""
+    x = operator.index(x)
+    if not -(1 << (bits - 1)) <= x < 1 << (bits - 1):
+        raise ValueError(f"{name}: {x} does not fit in {bits} bits")
+    return x
 
 
 def _share(delta, dims, row):
@@ -90,6 +99,9 @@ class RotaryTable:
             raise ValueError(f"unknown layout {layout!r}: half or interleaved")
         if scaling not in _SCALING:
             raise ValueError(f"unknown scaling {scaling!r}: None, linear, ntk or yarn")
+        rot_dim = _int(rot_dim, 32, "rot_dim")
+        if rot_dim > 1 << 20:
+            raise ValueError(f"rot_dim: {rot_dim} is beyond every head size")
         turns = (ctypes.c_uint64 * max(1, rot_dim // 2))()
         mag = ctypes.c_float()
         st = B.arf_rotary_turns(rot_dim, base, _SCALING[scaling], factor, original_length, beta_fast, beta_slow,
@@ -129,6 +141,8 @@ class KVCache:
             raise ValueError(f"k is on {k.device}, v on {v.device}: one CUDA device is needed")
         if k.stride(3) != 1 and k.shape[3] > 1:
             raise ValueError("the elements of a head must be contiguous")
+        for n, name in zip(k.shape, ("pages", "page tensor", "page tensor", "head_dim")):
+            _int(n, 32, name)
         pages, a, b, d = k.shape
         sp, sa, sb, _ = k.stride()
         (page_size, heads), (st, sh) = ((a, b), (sa, sb)) if layout == "nhd" else ((b, a), (sb, sa))
@@ -217,7 +231,8 @@ class PagePool:
     def __init__(self, num_pages: int, page_size: int):
         self.handle = ctypes.c_void_p()
         self.page_size = page_size
-        self._check(B.arf_pages_create(num_pages, page_size, self.handle), "arf_pages_create")
+        self._check(B.arf_pages_create(_int(num_pages, 32, "num_pages"), _int(page_size, 32, "page_size"), self.handle),
+                    "arf_pages_create")
 
     @staticmethod
     def _check(st, what):
@@ -226,23 +241,24 @@ class PagePool:
 
     def open(self, tokens: int = 0) -> int:
         seq = ctypes.c_int32()
-        self._check(B.arf_pages_open(self.handle, tokens, seq), "arf_pages_open")
+        self._check(B.arf_pages_open(self.handle, _int(tokens, 64, "tokens"), seq), "arf_pages_open")
         return seq.value
 
     def extend(self, seq: int, tokens: int = 1):
         """Returns the (src, dst) page copy to make first, or None."""
         src, dst = ctypes.c_int32(), ctypes.c_int32()
-        self._check(B.arf_pages_extend(self.handle, seq, tokens, src, dst), "arf_pages_extend")
+        self._check(B.arf_pages_extend(self.handle, _int(seq, 32, "sequence"), _int(tokens, 64, "tokens"), src, dst),
+                    "arf_pages_extend")
         return (src.value, dst.value) if src.value >= 0 else None
 
     def fork(self, seq: int) -> int:
         child = ctypes.c_int32()
-        self._check(B.arf_pages_fork(self.handle, seq, child), "arf_pages_fork")
+        self._check(B.arf_pages_fork(self.handle, _int(seq, 32, "sequence"), child), "arf_pages_fork")
         return child.value
 
     def free(self, seq: int) -> None:
         """Ends a sequence."""
-        self._check(B.arf_pages_close(self.handle, seq), "arf_pages_close")
+        self._check(B.arf_pages_close(self.handle, _int(seq, 32, "sequence")), "arf_pages_close")
 
     def compact(self):
         """Moves pages down so that those in use come first; returns (src,
@@ -267,13 +283,13 @@ class PagePool:
 
     def _size(self, seq):
         n, tokens = ctypes.c_int32(), ctypes.c_int64()
-        self._check(B.arf_pages_table(self.handle, seq, None, 0, n, tokens), "arf_pages_table")
+        self._check(B.arf_pages_table(self.handle, _int(seq, 32, "sequence"), None, 0, n, tokens), "arf_pages_table")
         return n.value, tokens.value
 
     def block_table(self, seqs, width: int | None = None):
         """(block_table [len(seqs), width], lens) as CPU int32 tensors for
         paged_decode; unused entries are -1."""
-        seqs = list(seqs)
+        seqs = [_int(s, 32, "sequence") for s in seqs]
         sizes = [self._size(s) for s in seqs]
         widest = max((n for n, _ in sizes), default=0)
         if width is not None and width < widest:

@@ -418,3 +418,23 @@ def test_shared_elements_are_found(seed):
     for delta in range(-inside - 3, inside + 4):
         assert _share(delta, dims, row) == bool(at & {x + delta for x in at}), (delta, dims, row)
     assert not _share(0, [(8, 0), (4, 2), (2, 2)], 2)
+
+
+def test_numbers_are_not_cut_off():
+    """Integers beyond the C types are refused, not taken modulo 2^32 or 2^64."""
+    for make in (lambda: arf.PagePool((1 << 32) + 4, 4), lambda: arf.PagePool(4, (1 << 32) + 4),
+                 lambda: arf.RotaryTable((1 << 32) + 8, device="cpu"), lambda: arf.RotaryTable((1 << 20) + 2, device="cpu"),
+                 lambda: arf.KVCache(*[torch.zeros(1, 1, 1, 8, dtype=torch.bfloat16).expand((1 << 32) + 4, -1, -1, -1)] * 2)):
+        with pytest.raises(ValueError):
+            make()
+    with arf.PagePool(8, 4) as pool:
+        s = pool.open(3)
+        big = s + (1 << 32)
+        for call in (lambda: pool.open((1 << 64) + 1), lambda: pool.extend(s, (1 << 64) + 1), lambda: pool.extend(big, 1),
+                     lambda: pool.fork(big), lambda: pool.free(big), lambda: pool.length(big), lambda: pool.pages(big),
+                     lambda: pool.block_table([big])):
+            with pytest.raises(ValueError):
+                call()
+        with pytest.raises(TypeError):
+            pool.open(2.0)
+        assert pool.length(s) == 3 and pool.free_pages == 7
