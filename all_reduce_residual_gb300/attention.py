@@ -23,6 +23,7 @@ count as modified in place.
 from __future__ import annotations
 
 import ctypes
+import math
 import operator
 import os
 
@@ -90,13 +91,18 @@ class RotaryTable:
     (i, i + rot_dim/2) or "interleaved" pairs (2i, 2i + 1). scaling: None,
     "linear", "ntk" or "yarn" with `factor`; original_length (the trained
     context), beta_fast and beta_slow are used by "yarn".
+
+    "yarn" is the formula of its paper: the ramp between the pairs that slow
+    down and those that do not is linear in the turns that a pair makes over
+    original_length, and cos and sin are multiplied by 0.1 ln(factor) + 1.
+    Models trained with another ramp (released code takes it linear in the
+    pair's index), another factor or none have other angles: from_frequencies
+    takes theirs.
     """
 
     def __init__(self, rot_dim: int, base: float = 10000.0, scaling=None, factor: float = 1.0,
                  original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, layout: str = "half",
                  device=None):
-        if layout not in ("half", "interleaved"):
-            raise ValueError(f"unknown layout {layout!r}: half or interleaved")
         if scaling not in _SCALING:
             raise ValueError(f"unknown scaling {scaling!r}: None, linear, ntk or yarn")
         rot_dim = _int(rot_dim, 32, "rot_dim")
@@ -108,12 +114,32 @@ class RotaryTable:
                                 turns, mag)
         if st != B.ARF_OK:
             raise B.ArfError(st, "arf_rotary_turns")
-        self._rot_dim, self._layout, self._magnitude = rot_dim, layout, mag.value
+        self._set(turns, mag.value, layout, device)
+
+    @classmethod
+    def from_frequencies(cls, frequencies, magnitude: float = 1.0, layout: str = "half", device=None):
+        """The table of a model's own frequencies: radians per position of
+        each pair (a sequence or tensor, taken in binary64; 2 len(frequencies)
+        leading elements of a head rotate), and a factor for cos and sin."""
+        w, magnitude = [float(x) for x in frequencies], float(magnitude)
+        if not 1 <= len(w) <= 1 << 19 or not all(map(math.isfinite, (*w, magnitude))):
+            raise ValueError("frequencies: a finite number for each of 1 to 2^19 pairs; magnitude: finite")
+        table = cls.__new__(cls)
+        # as a fraction of a turn times 2^64, whole turns dropped
+        turns = (ctypes.c_uint64 * len(w))(*(round(math.fmod(x / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for x in w))
+        table._set(turns, magnitude, layout, device)
+        return table
+
+    def _set(self, turns, magnitude, layout, device):
+        if layout not in ("half", "interleaved"):
+            raise ValueError(f"unknown layout {layout!r}: half or interleaved")
+        rot_dim = 2 * len(turns)
+        self._rot_dim, self._layout, self._magnitude = rot_dim, layout, magnitude
         # torch has no 64-bit unsigned type that kernels need here: the same bits as int64
         host = torch.frombuffer(turns, dtype=torch.int64)
         self._turns = host.clone() if device is not None and torch.device(device).type == "cpu" else \
             host.to(device if device is not None else torch.device("cuda", torch.cuda.current_device()))
-        self._struct = B.Rotary(self._turns.data_ptr(), rot_dim, int(layout == "interleaved"), mag.value)
+        self._struct = B.Rotary(self._turns.data_ptr(), rot_dim, int(layout == "interleaved"), magnitude)
         # what _torch_ops reads: the struct's address, and the device
         self._table_key = (ctypes.addressof(self._struct), self._turns.get_device())
 

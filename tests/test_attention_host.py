@@ -438,3 +438,21 @@ def test_numbers_are_not_cut_off():
         with pytest.raises(TypeError):
             pool.open(2.0)
         assert pool.length(s) == 3 and pool.free_pages == 7
+
+
+def test_table_of_given_frequencies():
+    for base, rot in ((10000.0, 64), (500000.0, 6)):
+        w = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+        a, b = arf.RotaryTable(rot, base=base, device="cpu"), arf.RotaryTable.from_frequencies(w, device="cpu")
+        # the same binary64 frequencies, a division and a product by 2^64 each
+        assert all(abs(x - y) <= abs(x) * 2.0 ** -50 + 1 for x, y in zip(a.turns.tolist(), b.turns.tolist()))
+        assert (b.rot_dim, b.layout, b.magnitude) == (rot, "half", 1.0) and b.struct.rot_dim == rot
+    t = arf.RotaryTable.from_frequencies(torch.tensor([-0.5, 0.0, 7.0], dtype=torch.float64), 0.75, "interleaved", "cpu")
+    want = [x / (2 * math.pi) % 1.0 for x in (-0.5, 0.0, 7.0)]  # whole turns drop out
+    got = [x % 2 ** 64 / 2.0 ** 64 for x in t.turns.tolist()]
+    assert all(abs(x - y) <= 2.0 ** -52 for x, y in zip(got, want))
+    assert t.struct.interleaved == 1 and t.struct.magnitude == 0.75 and t.rot_dim == 6
+    for bad in (dict(frequencies=[]), dict(frequencies=[1.0, math.inf]), dict(frequencies=[math.nan]),
+                dict(frequencies=[1.0], magnitude=math.inf), dict(frequencies=[1.0], layout="other")):
+        with pytest.raises(ValueError):
+            arf.RotaryTable.from_frequencies(**bad, device="cpu")

@@ -1178,3 +1178,23 @@ def test_keys_and_values_that_share_elements(ws):
     arf.rotary_append(ws, None, k, k, None, slots, None, cache)
     arf.copy_pages(ws, cache, [0], [1])
     assert torch.equal(base[1], base[0]) and torch.equal(base[0, :3], k) and torch.equal(base[0, page:page + 3], k)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_of_given_frequencies(ws, interleaved):
+    """Frequencies that no named scaling has: a ramp linear in the pair's
+    index between the pairs of 32 turns and of 1 turn, its factor given."""
+    rot, D, base, factor, length = 64, 80, 10000.0, 16.0, 4096
+    w = inv_freq(rot, base)
+    at = lambda turns: rot * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+    lo, hi = math.floor(at(32.0)), math.ceil(at(1.0))
+    keep = 1.0 - ((torch.arange(rot // 2, dtype=torch.float64) - lo) / (hi - lo)).clamp(0, 1)
+    w = w * (keep + (1.0 - keep) / factor)
+    pos = torch.randint(0, 60000, (50,), generator=gen(1), dtype=torch.int32)
+    q = randn((50, 3, D), BF16, 2)
+    for magnitude in (1.0, 0.1 * math.log(factor) + 1.0):
+        table = arf.RotaryTable.from_frequencies(w, magnitude, "interleaved" if interleaved else "half")
+        qo, _ = arf.rotary(ws, q.to(DEV), None, pos.to(DEV), table)
+        want, bound = ref.rotate(q, pos, w, rot, interleaved, magnitude)
+        ref.assert_close(qo, want, bound + ref.half_step(want, BF16))
+        assert same(qo[..., rot:], q[..., rot:])
