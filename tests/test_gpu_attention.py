@@ -1198,3 +1198,108 @@ def test_rotary_of_given_frequencies(ws, interleaved):
         want, bound = ref.rotate(q, pos, w, rot, interleaved, magnitude)
         ref.assert_close(qo, want, bound + ref.half_step(want, BF16))
         assert same(qo[..., rot:], q[..., rot:])
+
+
+# ---- the form with scratch, on several streams, threads and graphs ------------------
+
+
+def wide_batch(ws, lens, seed, Hkv=1, G=4, D=64, width=4000):
+    """A batch whose table is wide enough for the dealt form: (arguments of
+    paged_decode on the device, the expected result)."""
+    q, kp, vp, table, n = batch(lens, 16, Hkv, G, D, BF16, BF16, "nhd", seed=seed, width=width)
+    cache, size = arf.KVCache(kp.to(DEV), vp.to(DEV)), ctypes.c_size_t()
+    assert arf.arf_paged_decode_scratch_bytes(ws.handle, cache.struct, len(lens), Hkv * G, width, 0, size) == arf.ARF_OK
+    assert size.value > 0, "the form with scratch is meant"
+    return (q.to(DEV), cache, table.to(DEV), n.to(DEV)), ref.decode(q, kp, vp, "nhd", table, n, D ** -0.5)
+
+
+def test_decode_with_scratch_on_several_streams(ws):
+    cases = [wide_batch(ws, [5000, 17, 0, 300 + i], 10 * i) for i in range(4)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        got = [arf.paged_decode(ws, *args, stream=s) for s, (args, _) in zip(streams, cases)]
+    torch.cuda.synchronize()
+    for g, (_, want) in zip(got, cases):
+        ref.assert_decode(g, want, BF16)
+
+
+def test_decode_with_scratch_from_two_threads(ws):
+    import threading
+    cases, errors = [wide_batch(ws, [9000, 17, 0, 300 + i], 10 * i) for i in range(2)], []
+    torch.cuda.synchronize()
+
+    def work(args, want):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                got = [arf.paged_decode(ws, *args) for _ in range(50)]
+                s.synchronize()
+            for g in got[::7]:
+                ref.assert_decode(g, want, BF16)
+        except Exception as e:  # noqa: BLE001  (reported by the test's thread)
+            errors.append(e)
+    ts = [threading.Thread(target=work, args=c) for c in cases]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not errors, errors
+
+
+def test_graphs_with_scratch_share_a_workspace(ws):
+    """Two graphs captured with one workspace, replayed at the same time."""
+    cases = [wide_batch(ws, [9000, 17, 0, 4000 + i], 10 * i) for i in range(2)]
+    streams, graphs, outs = [torch.cuda.Stream() for _ in cases], [], []
+    for s, (args, _) in zip(streams, cases):
+        arf.paged_decode(ws, *args)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(arf.paged_decode(ws, *args))
+        graphs.append(g)
+    for it in range(10):
+        for o in outs:
+            o[0].fill_(5.0)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for s, g in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for o, (_, want) in zip(outs, cases):
+            ref.assert_decode(o, want, BF16, f"replay {it}")
+
+
+def check_before_window(ws, lens, page, D, cdt, layout, window, scratch):
+    """NaN in every row before the window, and no page at all (-1) where a
+    page lies wholly before it: neither is read, neither is counted."""
+    ks = 0.02 if cdt == E4M3 else 1.0
+    q, kp, vp, table, n = batch(lens, page, 1, 3, D, BF16, cdt, layout, seed=window, ks=ks, vs=ks)
+    want = ref.decode(q, kp, vp, layout, table, n, D ** -0.5, 0.0, window, ks, ks)
+    slot = torch.arange(table.shape[1] * page)
+    for p in (kp, vp):
+        x = p.view(torch.uint8) if cdt == E4M3 else p
+        x = x if layout == "nhd" else x.transpose(1, 2)
+        for b, m in enumerate(lens):
+            j = slot[: max(0, m - window)]
+            x[table[b, j // page].long(), j % page] = 0x7F if cdt == E4M3 else math.nan
+    for b, m in enumerate(lens):
+        table[b, : max(0, m - window) // page] = -1
+    cache, size = arf.KVCache(kp.to(DEV), vp.to(DEV), layout, ks, ks), ctypes.c_size_t()
+    assert arf.arf_paged_decode_scratch_bytes(ws.handle, cache.struct, len(lens), 3, table.shape[1], window,
+                                              size) == arf.ARF_OK and (size.value > 0) == scratch
+    got = arf.paged_decode(ws, q.to(DEV), cache, table.to(DEV), n.to(DEV), window=window)
+    ref.assert_decode(got, want, BF16, f"{page} {window} {D}")
+    assert arf.bad_indices(ws) == 0
+
+
+@pytest.mark.parametrize("page", [16, 5, 64])
+@pytest.mark.parametrize("window", [1, 15, 33, 100])
+def test_decode_reads_nothing_before_the_window(ws, page, window):
+    for D, cdt, layout in ((64, BF16, "nhd"), (128, E4M3, "hnd"), (256, BF16, "nhd")):
+        check_before_window(ws, [300, 33, 1, 64, window, window + 1, 0], page, D, cdt, layout, window, False)
+
+
+@pytest.mark.parametrize("page", [16, 5, 64])
+def test_decode_with_scratch_reads_nothing_before_the_window(ws, page):
+    check_before_window(ws, [30011, 9000, 0, 9001, 9077], page, 64, BF16, "nhd", 9000, True)
+    check_before_window(ws, [30011, 9000, 0, 9001, 9077], page, 128, E4M3, "hnd", 9000, True)
