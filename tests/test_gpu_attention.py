@@ -1301,5 +1301,5 @@ def test_decode_reads_nothing_before_the_window(ws, page, window):
 
 @pytest.mark.parametrize("page", [16, 5, 64])
 def test_decode_with_scratch_reads_nothing_before_the_window(ws, page):
-    check_before_window(ws, [30011, 9000, 0, 9001, 9077], page, 64, BF16, "nhd", 9000, True)
-    check_before_window(ws, [30011, 9000, 0, 9001, 9077], page, 128, E4M3, "hnd", 9000, True)
+    check_before_window(ws, [40011, 20000, 0, 20001, 20077], page, 64, BF16, "nhd", 20000, True)
+    check_before_window(ws, [40011, 20000, 0, 20001, 20077], page, 128, E4M3, "hnd", 20000, True)
