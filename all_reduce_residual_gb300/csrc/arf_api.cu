@@ -24,7 +24,10 @@ struct arf_workspace {
     std::mutex mu;
     std::map<std::tuple<int, int, int64_t, int64_t, int>, arf_plan_t> plans;
     std::atomic<int> last_err{0};
-    int decode_cluster = 1;  // largest cluster of the decode attention kernels
+    // The decode attention's kernels: the largest cluster they can run in, or
+    // the error that setting them up returned.
+    int decode_cluster = 1;
+    cudaError_t decode_err = cudaSuccess;
     unsigned int* wait_timeouts = nullptr;  // device counter of the bulk kernel's given-up waits
     // Device address of the staging array of arf_run_host_static on this
     // workspace's device, looked up at creation (arf_static.cu), or the
@@ -190,7 +193,13 @@ extern "C" arf_status_t arf_workspace_create(int device, arf_workspace_t* ws_out
         const int dyn = smem - arf::kAsyncStaticSmem;
         e = arf::configure_kernels_bf16(cl != 0, dyn);
         if (e == cudaSuccess) e = arf::configure_kernels_fp16(cl != 0, dyn);
-        if (e == cudaSuccess) e = arf::configure_decode(cl != 0, smem, &ws->decode_cluster);
+    }
+    if (e == cudaSuccess) {
+        // Set up here and not by the first call, which may be captured: 1.6 of
+        // the 24 ms that a process's first workspace takes, 0.02 of 0.15 for a
+        // later one. A failure only disables arf_paged_decode.
+        ws->decode_err = arf::configure_decode(cl != 0, smem, &ws->decode_cluster);
+        if (ws->decode_err != cudaSuccess) (void)cudaGetLastError();
     }
     if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&ws->wait_timeouts), 256);
     if (e == cudaSuccess) e = cudaMemset(ws->wait_timeouts, 0, 256);
@@ -1179,6 +1188,9 @@ arf_status_t workspace_check_device(arf_workspace_t ws, cudaStream_t stream) {
 const arf_device_caps_t& workspace_caps(arf_workspace_t ws) { return ws->caps; }
 unsigned int* workspace_bad_counter(arf_workspace_t ws) { return ws->wait_timeouts + kBadIndexWord; }
 unsigned int* workspace_timeout_counter(arf_workspace_t ws) { return ws->wait_timeouts; }
+arf_status_t workspace_check_decode(arf_workspace_t ws) {
+    return ws->decode_err == cudaSuccess ? ARF_OK : cuda_fail(ws, ws->decode_err);
+}
 int workspace_decode_cluster(arf_workspace_t ws) { return ws->decode_cluster; }
 
 __global__ void fill_pointer_array(const void** array, const char* first, int64_t stride, int W) {

@@ -131,6 +131,8 @@ extern "C" arf_status_t arf_paged_decode_scratch_bytes(arf_workspace_t ws, const
     const arf_status_t st = check_cache(cache);
     if (st != ARF_OK) return st;
     if (heads % cache->kv_heads != 0) return ARF_ERR_INVALID_ARG;
+    const arf_status_t ready = workspace_check_decode(ws);
+    if (ready != ARF_OK) return ready;
     const int group = heads / cache->kv_heads;
     const int nt = groups_of(cache->head_dim, group);
     DecodeKernels k;
@@ -189,6 +191,7 @@ extern "C" arf_status_t arf_paged_decode(arf_workspace_t ws, const arf_kv_cache_
     if (B > 1 && table_stride > kMaxExtent / B) return ARF_ERR_UNSUPPORTED;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     st = workspace_check_device(ws, stream);
+    if (st == ARF_OK) st = workspace_check_decode(ws);
     if (st != ARF_OK || B == 0) return st;
     const int cap_tokens = token_cap(table_width, cache->page_size);
     // units of a sequence, and of a CTA, are 32-bit numbers

@@ -175,6 +175,7 @@ unsigned int* workspace_timeout_counter(arf_workspace_t ws);
 // than 8 CTAs where the device has them, up to `max_smem` bytes per CTA. The
 // largest cluster that can be resident in *max_cluster, kept by the workspace.
 cudaError_t configure_decode(bool clusters, int max_smem, int* max_cluster);
+arf_status_t workspace_check_decode(arf_workspace_t ws);  // CUDA if that failed
 int workspace_decode_cluster(arf_workspace_t ws);
 
 // The staging array of arf_run_host_static (arf_static.cu): its device

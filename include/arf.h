@@ -145,10 +145,13 @@ typedef struct arf_workspace* arf_workspace_t;
  * from these, as flashinfer PR #1507 "update allreduce to match trtllm",
  * Highlights, derives threads_per_block and cluster_size from the SM count).
  * Makes `device` current on the calling thread. Allocates the workspace's
- * only device memory here: 256 bytes holding the bulk kernel's wait-timeout
- * counter (arf_workspace_wait_timeouts); no later call allocates for it.
+ * only device memory here: 256 bytes holding the counters of waits that ran
+ * out (arf_workspace_wait_timeouts) and of skipped accesses
+ * (arf_workspace_bad_indices); no later call allocates for it.
  * Also creates the two non-blocking streams and four events of
  * arf_run_host's pipelined form; arf_workspace_destroy releases them all.
+ * Sets up the kernels; where that fails for those of the decode attention
+ * alone, arf_paged_decode and arf_paged_decode_scratch_bytes return CUDA.
  * Errors: ws_out NULL -> INVALID_ARG; no such device or a CUDA failure -> CUDA. */
 arf_status_t arf_workspace_create(int device, arf_workspace_t* ws_out);
 
