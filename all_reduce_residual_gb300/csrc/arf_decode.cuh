@@ -37,10 +37,10 @@
 //
 // Measured, in a graph: 83 us for 128 sequences of up to 4096 tokens, 16 / 4
 // heads of 128, bf16 (507 MB, 6.1 TB/s; a read-only pass takes 69 us, the SMs
-// end about 73 to 79 us after the start, the join and the launches take 5); 64
-// us for 48 of up to 30011 tokens, 16 / 2 heads, e4m3 (371 MB, 5.8 TB/s); 41
-// us for two of 262001, 8 / 1 heads, fp16 (217 MB); 56 us for 24 with a window
-// of 4096, 8 / 4 heads of 256 (318 MB); 4.9 us for one of 517.
+// end about 73 to 79 us after the start, the join and the launches take 5); 65
+// us for 48 of up to 30011 tokens, 16 / 2 heads, e4m3 (371 MB, 5.7 TB/s); 41.5
+// us for two of 262001, 8 / 1 heads, fp16 (217 MB); 56.5 us for 24 with a window
+// of 4096, 8 / 4 heads of 256 (318 MB); 4.8 us for one of 517.
 #pragma once
 
 #include <type_traits>
@@ -616,7 +616,8 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
     constexpr int LO = ES == 2 ? 1 : 0;
     // P as the sum of two 16-bit values (2^-16 of it, or 2^-22 in fp16): one
     // alone would be as large an error as the rounding of out for values of
-    // the cache's type, and an eighth of it for bf16 out of an fp16 product.
+    // the cache's type, and an eighth of it for bf16 out of an fp16 product
+    // (where the second costs 1.7 us of the 64.6 of the e4m3 batch above).
     float o[1 + LO][NT][KS][4];
     // The softmax's reference, in units of log2, per head: kRoom below the
     // maximum when it was last set. It is set anew only when a score exceeds

@@ -6,8 +6,9 @@
 // fixed-point fraction of a turn, so f_i * p modulo 2^64 is one integer
 // multiplication that drops whole turns exactly. Its upper 32 bits give the
 // nearest quarter turn and a rest of at most an eighth, whose sine and cosine
-// are short Taylor polynomials. Angles of positions near 2^31 are as exact as
-// those near 0 without a 64-bit float instruction.
+// are short Taylor polynomials. No 64-bit float instruction is needed at any
+// position, and what a far one's angle is off by is the table's own error, the
+// frequencies' in binary64 (2^-53 of the angle, or a few of those).
 //
 // What bounds it. About 1 flop per byte: HBM for prompts, launch latency for
 // decode steps. Split: a lane of a block owns one unit of a token's heads
@@ -16,11 +17,11 @@
 // A thread issues all its loads; while they are under way each warp takes two
 // of the 8 cosines and sines of every lane's unit, and the four warps share
 // them through shared memory. HPT is kManyHeads for many tokens and 1 where
-// that would leave SMs without threads. Measured, in a graph: 26.2 us for 8191
+// that would leave SMs without threads. Measured, in a graph: 26.1 us for 8191
 // tokens of 32 + 8 heads of 128, half rotated, fp16 (6.4 TB/s; with every
 // thread taking its own 8 sines and four heads 28.3, a block per token with a
 // table of sines 37.2); 11.3 us for the append of 5851 tokens of 16 + 2 x 4
-// heads (6.4 TB/s); 2.0 us for 128 tokens of 16 + 4.
+// heads (6.3 TB/s), 11.2 to e4m3 pages (5.9 TB/s); 1.9 us for 128 tokens of 16 + 4.
 #include <algorithm>
 #include <climits>
 

@@ -521,9 +521,11 @@ typedef enum arf_rope_scaling {
 /* Host: the angle of every pair per position as a fraction of a turn in
  * 64-bit fixed point, turns_out[i] = round(w_i / (2 pi) * 2^64), i < rot_dim
  * / 2, and the factor for cos and sin in *magnitude_out. The kernels
- * multiply by the position modulo 2^64, which drops whole turns exactly: the
- * angle of a far position is as exact as that of a near one (up to
- * |position| * 2^-53 of w_i itself). Any table made by other means works too.
+ * multiply by the position modulo 2^64, which drops whole turns exactly: what
+ * grows with the position is the table's own error alone (w_i in binary64:
+ * |position| * w_i * 2^-53 radians, or a few of those). Any table made by other
+ * means works too: models trained with other frequencies than these (YARN's
+ * ramp over the pairs' indices, for one) need theirs.
  * Errors: NULL, rot_dim < 2 or odd, base <= 1, factor < 1, original_length
  * < 1 or beta_fast <= beta_slow (YARN), rot_dim < 4 (NTK), a non-finite
  * value or an unknown scaling -> INVALID_ARG. */
@@ -550,7 +552,8 @@ typedef struct arf_rotary {
  * T == 0 launches nothing. Errors: rot_dim > D or odd, heads < 1, q_out and q
  * of different head counts, in place with different strides -> INVALID_ARG;
  * odd pointers, T or a stride beyond 2^40 / extents, D beyond 2^20, more than
- * 2^17 heads -> UNSUPPORTED. */
+ * 262140 heads of q, k and (where a cache is written) v together, or twice as
+ * many in 16-byte vectors -> UNSUPPORTED. */
 arf_status_t arf_rotary(arf_workspace_t ws, const arf_rotary_t* rot, const int32_t* positions,
                         int64_t T, int D, arf_dtype_t dtype,
                         const arf_heads_t* q, const arf_heads_t* q_out,
