@@ -79,6 +79,15 @@ def _share(delta, dims, row):
     return meets(delta, reach, dims)
 
 
+def _base(t):
+    """The tensor that t is a view of, which shares its version counter (one
+    for all layers where they are views of one tensor), or t."""
+    try:
+        return t._base if t._is_view() else t
+    except RuntimeError:  # a view that autograd does not follow
+        return t
+
+
 def _fixed(name):
     return property(lambda self: getattr(self, "_" + name))
 
@@ -163,6 +172,8 @@ class KVCache:
             raise ValueError("k and v: two page tensors of equal shape, strides and dtype")
         if k.dtype not in _CACHE_DTYPE:
             raise ValueError(f"unsupported cache dtype {k.dtype}: bf16, fp16 or float8_e4m3fn")
+        if k.requires_grad or v.requires_grad:
+            raise ValueError("k and v: pages that require a gradient, which no call records: detach them")
         if k.device != v.device or not k.is_cuda:
             raise ValueError(f"k is on {k.device}, v on {v.device}: one CUDA device is needed")
         if k.stride(3) != 1 and k.shape[3] > 1:
@@ -180,8 +191,9 @@ class KVCache:
         # them would leave which of the two is there to chance
         es = k.element_size()
         shared = _share(v.data_ptr() - k.data_ptr(), [(sp * es, pages), (sa * es, a), (sb * es, b)], d * es)
-        # what _torch_ops reads: the struct's address, the device, the tensors, whether they may be written
-        self._cache_key = (ctypes.addressof(self._struct), k.get_device(), k, v, not shared)
+        # what _torch_ops reads: the struct's address, the device, whether the
+        # pages may be written, and the tensors whose versions count that
+        self._cache_key = (ctypes.addressof(self._struct), k.get_device(), not shared, _base(k), _base(v))
 
     # the struct holds the pages' addresses: a cache of other pages is made anew
     k, v, layout, num_pages, page_size, kv_heads, head_dim, struct = map(

@@ -7,7 +7,7 @@
 // these calls per layer, with six to eight tensors each. On the host of a
 // GB300 the marshalling of one call in Python took 22 to 28 us, ten times
 // the kernel's time; here a call takes 2.4 us with its outputs given (1.6 of
-// them the launch), 3.8 with outputs made; a page copy 2.8, and 0.08 more per
+// them the launch), 3.8 with outputs made; a page copy 2.9, and 0.04 more per
 // layer beyond the first.
 #include <ATen/core/Tensor.h>
 #include <c10/core/Allocator.h>
@@ -171,8 +171,9 @@ Pair empty_pair(const Stream& stream, at::IntArrayRef size0, ScalarType dtype0, 
 }
 
 // The C struct behind a handle object of attention.py: its attribute `key`
-// is a tuple (address of the struct, device index; of a cache also its keys,
-// its values, and whether they may be written).
+// is a tuple (address of the struct, device index; of a cache also whether it
+// may be written, and the tensors whose versions count what is written to its
+// keys and to its values).
 PyObject* kCacheKey = nullptr;  // the attributes' names, interned at import
 PyObject* kTableKey = nullptr;
 
@@ -199,19 +200,16 @@ Handle handle_of(PyObject* o, PyObject* name, Py_ssize_t size, const char* what,
 struct Cache {
     const arf_kv_cache_t* c;
     PyObject* key;
-    const Tensor& pages(int i) const { return THPVariable_Unpack(PyTuple_GET_ITEM(key, 2 + i)); }
     void check_writable() const {
-        TORCH_CHECK_VALUE(PyTuple_GET_ITEM(key, 4) == Py_True,
+        TORCH_CHECK_VALUE(PyTuple_GET_ITEM(key, 2) == Py_True,
                           "the KVCache's keys and values share elements: it can only be read");
     }
-    void written_to() const { written(pages(0)), written(pages(1)); }
+    PyObject* base(int i) const { return PyTuple_GET_ITEM(key, 3 + i); }
     const arf_kv_cache_t* operator->() const { return c; }
 };
 Cache cache_of(PyObject* o, int device) {
     const Handle h = handle_of(o, kCacheKey, 5, "KVCache", device);
-    const Cache cache = {reinterpret_cast<const arf_kv_cache_t*>(h.at), h.key};
-    for (int i = 0; i < 2; ++i) no_gradient(tensor(PyTuple_GET_ITEM(h.key, 2 + i), "the KVCache"), "the KVCache");
-    return cache;
+    return {reinterpret_cast<const arf_kv_cache_t*>(h.at), h.key};
 }
 const arf_rotary_t* rotary_of(PyObject* o, int device) {
     return reinterpret_cast<const arf_rotary_t*>(handle_of(o, kTableKey, 2, "RotaryTable", device).at);
@@ -325,7 +323,7 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                              has_q ? &qo : nullptr, &kh, &vh, cache.c, stream.raw());
     if (r != ARF_OK) return status(r);
     written(a[9]);
-    cache.written_to();
+    for (int i = 0; i < 2; ++i) written(tensor(cache.base(i), "pages"));
     if (q_out.defined()) return THPVariable_Wrap(std::move(q_out));
     PyObject* out = has_q ? a[9] : Py_None;
     Py_INCREF(out);
@@ -465,8 +463,11 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Stream stream(a[5], device);
     const arf_status_t r = arf_copy_pages(workspace(a[0]), caches.data(), (int)count, src.data(), dst.data(),
                                           (int)src.size(), stream.raw());
-    if (r == ARF_OK)
-        for (const Cache& cache : handles) cache.written_to();
+    if (r != ARF_OK) return status(r);
+    PyObject* last[2] = {nullptr, nullptr};  // layers are often views of one tensor
+    for (const Cache& cache : handles)
+        for (int i = 0; i < 2; ++i)
+            if (cache.base(i) != last[i]) written(tensor(last[i] = cache.base(i), "pages"));
     return status(r);
     END_HANDLE_TH_ERRORS
 }

@@ -1109,11 +1109,8 @@ def test_gradients_are_refused(ws):
              lambda: arf.rotary(ws, q, k, pos, rot, q_out=grad(q)), lambda: arf.rotary(ws, q * grad(q), None, pos, rot),
              lambda: arf.rotary_append(ws, q, k, grad(k), pos, pos.long(), rot, cache),
              lambda: arf.rotary_append(ws, q, grad(k), k, pos, pos.long(), rot, cache),
-             lambda: arf.rotary_append(ws, q, k, k, pos, pos.long(), rot, arf.KVCache(kp, grad(vp))),
              lambda: arf.paged_decode(ws, grad(q), cache, table, pos), lambda: arf.paged_decode(ws, q, cache, table, pos, lse=grad(lse)),
-             lambda: arf.paged_decode(ws, q, cache, table, pos, out=grad(q)),
-             lambda: arf.paged_decode(ws, q, arf.KVCache(grad(kp), vp), table, pos),
-             lambda: arf.copy_pages(ws, [cache, arf.KVCache(kp, grad(vp))], [0], [1])]
+             lambda: arf.paged_decode(ws, q, cache, table, pos, out=grad(q))]
     for call in calls:
         with pytest.raises(ValueError, match="gradient"):
             call()
@@ -1121,6 +1118,9 @@ def test_gradients_are_refused(ws):
         with off():
             for call in calls:
                 call()
+    for pages_ in ((kp, grad(vp)), (grad(kp), vp), (grad(kp)[:1], vp[:1])):
+        with pytest.raises(ValueError, match="gradient"):
+            arf.KVCache(*pages_)
 
 
 def test_what_a_call_writes_counts_as_modified(ws):
@@ -1146,6 +1146,12 @@ def test_what_a_call_writes_counts_as_modified(ws):
         cache = arf.KVCache(*pages_)
         stale(pages_[i], lambda: arf.rotary_append(ws, None, k, k, None, pos.long(), None, cache))
         stale(pages_[i], lambda: arf.copy_pages(ws, [cache], [0], [1]))
+        # views of one tensor, separate tensors and other views of both, in one call
+        both, views = torch.zeros(2, 2, 2, 16, 2, 64, dtype=BF16, device=DEV), pages_[i].detach()
+        many = [arf.KVCache(both[0, 0], both[0, 1]), cache, arf.KVCache(both[1, 0], both[1, 1])]
+        stale(both, lambda: arf.copy_pages(ws, many, [0], [1]))
+        stale(pages_[i], lambda: arf.copy_pages(ws, many, [0], [1]))
+        stale(pages_[i], lambda: arf.copy_pages(ws, arf.KVCache(views, torch.zeros_like(views)), [0], [1]))
     out, lse = torch.zeros_like(q), torch.zeros(2, 4, device=DEV)
     stale(out, lambda: arf.paged_decode(ws, q, cache, pos[:, None], pos, out=out))
     stale(lse, lambda: arf.paged_decode(ws, q, cache, pos[:, None], pos, lse=lse))
