@@ -96,13 +96,16 @@ struct Pack8<__half> {
 };
 
 // ---------------------------------------------------------------------------
-// Memory access. Partials are read exactly once: the read-only path without
-// L1 allocation. gamma is re-read by every row: the default cached read-only
-// load.
+// Memory access. Partials are read exactly once: without L1 allocation, and
+// coherent, not by .nc loads: a programmatic dependent is resident while the
+// launch before it may still be writing them (measured level with .nc at every
+// size of the sweep). Their addresses come out of shared memory behind the
+// prologue's wait, so no load moves above it. gamma, a weight that no launch
+// writes, is re-read by every row: the default cached read-only load.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint4 ld_once(const uint4* p) {
     uint4 v;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
         : "l"(p));
     return v;
@@ -111,17 +114,18 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) {
 // ld_once whose issue order the compiler keeps (volatile).
 __device__ __forceinline__ uint4 ld_once_ordered(const uint4* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
 }
 
 // The residual may be overwritten by this kernel (residual_out == residual):
-// a coherent load, issued by the thread that later writes the same chunk.
+// a coherent load, issued by the thread that later writes the same chunk. Its
+// address is a launch parameter's: volatile keeps it behind the prologue's wait.
 __device__ __forceinline__ uint4 ld_resid(const uint4* p) {
     uint4 v;
-    asm("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
         : "l"(p));
     return v;
@@ -366,7 +370,7 @@ __device__ __forceinline__ void issue_row(uint4 (&L)[VPT][WS + 1], const uint4* 
                                      : "=r"(L[k][r].x), "=r"(L[k][r].y), "=r"(L[k][r].z), "=r"(L[k][r].w)
                                      : "l"(src));
                     else
-                        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(L[k][r].x), "=r"(L[k][r].y), "=r"(L[k][r].z), "=r"(L[k][r].w)
                                      : "l"(src));
                 }
@@ -386,7 +390,7 @@ __device__ __forceinline__ void issue_row(uint4 (&L)[VPT][WS + 1], const uint4* 
 #pragma unroll
                 for (int r = 0; r < WS; ++r) {
                     const uint4* pp = s_ptr[r] + pbase + c;
-                    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(L[k][r].x), "=r"(L[k][r].y), "=r"(L[k][r].z), "=r"(L[k][r].w)
                                  : "l"(pp));
                 }

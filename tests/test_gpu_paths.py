@@ -769,3 +769,42 @@ def test_outputs_on_another_stream_are_not_memory_in_use(ws):
         assert torch.equal(out, want) and torch.equal(ro, want_ro)
     assert {seg["stream"] for seg in torch.cuda.memory_snapshot() for t in got[0]
             if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]} == {s.cuda_stream}
+
+
+@pytest.mark.parametrize("W,M,H", [(2, 8, 1024), (3, 8, 1024), (8, 4, 7168), (2, 16, 4096), (2, 3, 1001), (4, 64, 2048)])
+def test_replayed_dependent_launches_read_what_the_one_before_wrote(ws, W, M, H):
+    """A chain of dependent launches in one graph: each one's first partial and
+    residual are the outputs of the launch before it, with other data in every
+    replay. Bitwise against the same chain without dependent launches."""
+    P = [torch.zeros(M, H, dtype=torch.bfloat16, device="cuda:0") for _ in range(W)]
+    R, G = torch.zeros_like(P[0]), torch.ones(H, dtype=torch.bfloat16, device="cuda:0")
+
+    def buffers():
+        """(out, residual_out, pointers of the partials) of six launches."""
+        made, first = [], P[0]
+        for _ in range(6):
+            made.append((torch.empty_like(R), torch.empty_like(R), arf.pointer_array([first, *P[1:]])))
+            first = made[-1][0]
+        return made
+
+    def chain(pdl, bufs):
+        first, residual = P[0], R
+        for out, ro, ptrs in bufs:
+            arf.run(ws, "rmsnorm", [first, *P[1:]], residual, G, 1e-6, out=out, residual_out=ro, ptrs=ptrs, pdl=pdl)
+            first, residual = out, ro
+
+    here, there = buffers(), buffers()
+    chain(True, here)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain(True, here)
+    for it in range(10):
+        gen = torch.Generator("cuda:0").manual_seed(it)
+        for t in (*P, R):
+            t.normal_(generator=gen)
+        g.replay()
+        chain(False, there)
+        torch.cuda.synchronize()
+        for (a, b, _), (c, d, _) in zip(here, there):
+            assert torch.equal(a, c) and torch.equal(b, d), f"replay {it}"
